@@ -350,6 +350,151 @@ dpo_status dpo_shard_backward(const dpo_batch* batch, const dpo_vocab_shard* sha
 dpo_status dpo_logits_mean(const dpo_batch* batch, int32_t layout, float* means, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* ---- Token statistics ------------------------------------------------------
+ * For every scored position (or given row), from one pass over the vocabulary and
+ * without forming the logits z = h . W^T:
+ *   lse     = log sum_v exp(z_v)
+ *   logp    = z_y - lse, y the given token
+ *   entropy = -sum_v p_v log p_v, p = softmax(z), in nats
+ *   top     = the n_top largest z: their ids and log-probs z - lse, in falling order,
+ *             equal logits by rising id
+ * (dpo_seq_logprobs' forward with what monitoring and serving ask for beside the target's
+ * log-prob.) The gradient of the log-probs is dpo_backward on the lse_state written here;
+ * the entropy and the alternatives are metrics and have none. The same inputs give the same
+ * bits on every run.
+ *   Any pointer may be NULL: that value is not wanted. top_ids and top_logp are [n, n_top],
+ *   n_top in 0 .. DPO_MAX_TOP; with n_top > 0 both are required.
+ *   A row with fewer than n_top logits above -1e30 (a small vocabulary, infinities) ends in
+ *   id -1, log-prob -inf. A NaN logit makes the row's lse, logp and entropy NaN and is no
+ *   alternative. A token outside [0, V) is a bad target: logp 0, the status word as for
+ *   dpo_seq_logprobs; the other values of its row do not depend on it. */
+#define DPO_MAX_TOP 32
+typedef struct {
+  float* logp;        /* device [n] or NULL                                              */
+  float* entropy;     /* device [n] or NULL                                              */
+  float* lse_state;   /* device [n] or NULL: what dpo_backward reads                     */
+  int32_t n_top;      /* alternatives per position, 0 .. DPO_MAX_TOP                     */
+  int32_t* top_ids;   /* device [n, n_top]                                               */
+  float* top_logp;    /* device [n, n_top]                                               */
+} dpo_token_stats_out;
+
+/* Workspace bytes of dpo_token_stats for this batch and n_top; a workspace of at least
+ * *min_bytes (may be NULL) makes it run in several chunks of positions, with the same
+ * results. Pure host function. */
+dpo_status dpo_token_stats_size(const dpo_batch* batch, int32_t n_top, size_t* bytes,
+                                size_t* min_bytes);
+
+/* Statistics of every scored position of a batch (n = Nc, in row order, the order of
+ * lse_state), and per-row sums.
+ *   seq_logp  device [R] fp32 or NULL, out: as dpo_seq_logprobs
+ *   ws        device workspace, >= min_bytes, 256-byte aligned
+ * Errors: those of dpo_seq_logprobs; DPO_ERR_INVALID_ARG for NULL out, n_top out of range or
+ * a missing top pointer. */
+dpo_status dpo_token_stats(const dpo_batch* batch, const dpo_token_stats_out* out,
+                           float* seq_logp, void* ws, size_t ws_bytes, void* stream);
+
+/* n independent hidden rows: the last token of each of n sequences in a serving step. */
+typedef struct {
+  int32_t n;               /* rows, 0 <= n <= 2^30                                       */
+  int32_t d;               /* as in dpo_batch                                            */
+  int32_t V;               /* as in dpo_batch                                            */
+  int32_t dtype;           /* dpo_dtype of H and W                                       */
+  const void* H;           /* device, n rows of d values, 16-byte aligned                */
+  int64_t h_stride;        /* values between rows' starts, >= d, a multiple of 8         */
+  const void* W;           /* device [V, d] row-major, 16-byte aligned                   */
+  const int32_t* tokens;   /* device [n] given tokens, or NULL when logp is NULL         */
+} dpo_token_rows;
+
+/* As dpo_token_stats_size and dpo_token_stats, for rows (H, W and tokens are not read by the
+ * size call and may be NULL there). n = 0 does nothing. DPO_ERR_UNSUPPORTED for an h_stride
+ * that is not a multiple of 8. */
+dpo_status dpo_token_stats_rows_size(const dpo_token_rows* rows, int32_t n_top, size_t* bytes,
+                                     size_t* min_bytes);
+dpo_status dpo_token_stats_rows(const dpo_token_rows* rows, const dpo_token_stats_out* out,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 8-bit activation checkpoints ------------------------------------------
+ * rows x d activations held between forward and backward in 8 bits and 1/32: blocks of 32
+ * along each row (the last block of a row may be shorter) share a scale 2^E with E the
+ * smallest integer >= -126 such that max |x| <= 127 * 2^E; a value is held as the integer
+ * rint(x * 2^-E), half to even, cut to +-127 (only values next to the largest finite number
+ * reach the cut). Every step but the rounding is exact: |x~ - x| <= 2^(E-1), and x~ = code *
+ * 2^E is exact in bf16 too. A block that holds an infinity or a NaN reads back as NaN. */
+#define DPO_CHECKPOINT_BLOCK 32
+typedef struct {
+  int8_t* codes;      /* device [rows, d], 16-byte aligned                               */
+  uint8_t* scales;    /* device [rows, ceil(d / 32)]: E + 127, or 255 for a NaN block    */
+} dpo_checkpoint;
+
+/* Hold x (rows of d values of `dtype`, DPO_BF16 or DPO_F32, x_stride values apart) in `out`,
+ * and read a checkpoint back into y. d a multiple of 8, 8 <= d <= 65536, strides >= d and
+ * multiples of 8, pointers 16-byte aligned; rows >= 0 (0 does nothing). Values of y between
+ * the rows (y_stride > d) are not written. */
+dpo_status dpo_checkpoint_pack(int32_t dtype, int32_t rows, int32_t d, const void* x,
+                               int64_t x_stride, const dpo_checkpoint* out, void* stream);
+dpo_status dpo_checkpoint_unpack(int32_t dtype, int32_t rows, int32_t d,
+                                 const dpo_checkpoint* from, void* y, int64_t y_stride,
+                                 void* stream);
+
+/* ---- The norm before the head ----------------------------------------------
+ * The model's final norm, whose output is the head's H and whose gradient starts at the dH
+ * that dpo_backward writes:
+ *   layer  mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps)
+ *   rms    mu = 0,       r = 1 / sqrt(mean(x^2) + eps)
+ *   xh = (x - mu) r,  y = xh * weight + bias
+ * and with g = dy * weight, over the d values of a row:
+ *   dx = r (g - c1 - xh c2),  c1 = mean(g) (layer; 0 for rms),  c2 = mean(g xh)
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ * Statistics and sums are fp32, in a fixed order: the same inputs give the same bits. */
+typedef enum { DPO_NORM_LAYER = 0, DPO_NORM_RMS = 1 } dpo_norm_kind;
+
+typedef struct {
+  int32_t kind;               /* dpo_norm_kind                                           */
+  int32_t dtype;              /* DPO_BF16 or DPO_F32: type of x, y and dx                */
+  int32_t weight_dtype;       /* type of weight and bias                                 */
+  int32_t rows;               /* >= 0 (0: nothing, but for zeroed weight gradients)      */
+  int32_t d;                  /* a multiple of 8, 8 <= d <= 65536                        */
+  float eps;                  /* >= 0, finite; the forward's only                        */
+  const void* x;              /* device, rows of d values; NULL when `from` is set       */
+  int64_t x_stride;           /* values between rows' starts, >= d, a multiple of 8      */
+  const dpo_checkpoint* from; /* read x from this checkpoint instead, or NULL            */
+  const void* weight;         /* device [d] or NULL (ones)                               */
+  const void* bias;           /* device [d] or NULL (zeros)                              */
+} dpo_norm;
+
+/* y = norm(x). Device pointers are 16-byte aligned (mean and rstd 4-byte).
+ *   y      rows of d values of norm->dtype, y_stride apart; y may be x itself (same stride)
+ *   mean   device [rows] fp32 or NULL (NULL for rms)
+ *   rstd   device [rows] fp32 or NULL
+ *   save   also hold x in this checkpoint, or NULL; not together with `from`
+ * With `from` the checkpoint's values take x's place, the statistics too: it forms H again
+ * for the backward without the forward's x. */
+dpo_status dpo_norm_forward(const dpo_norm* norm, void* y, int64_t y_stride, float* mean,
+                            float* rstd, const dpo_checkpoint* save, void* stream);
+
+typedef struct {
+  const float* mean;   /* device [rows] from the forward; NULL for rms                   */
+  const float* rstd;   /* device [rows] from the forward                                 */
+  const void* dy;      /* device, rows of d values of dy_dtype, dy_stride apart          */
+  int32_t dy_dtype;    /* DPO_BF16, or DPO_F32 (dpo_backward's dH)                       */
+  int64_t dy_stride;
+  void* dx;            /* device, rows of d values of norm->dtype, or NULL; may be dy
+                          itself (same type and stride)                                  */
+  int64_t dx_stride;
+  float* dweight;      /* device [d] fp32 or NULL                                        */
+  float* dbias;        /* device [d] fp32 or NULL                                        */
+  int32_t accumulate;  /* 1: dweight and dbias are added to instead of written           */
+} dpo_norm_grads;
+
+/* Workspace bytes of dpo_norm_backward. Pure host function. */
+dpo_status dpo_norm_workspace_size(int32_t rows, int32_t d, size_t* bytes);
+
+/* The gradients of dpo_norm_forward at x, or, with norm->from, at the values a checkpoint
+ * holds. eps and bias are not read. Buffers that overlap otherwise than named above are
+ * refused (DPO_ERR_INVALID_ARG). ws: device workspace, 256-byte aligned. */
+dpo_status dpo_norm_backward(const dpo_norm* norm, const dpo_norm_grads* grads, void* ws,
+                             size_t ws_bytes, void* stream);
+
 /* Size of the scratch array built into the library for dpo_seq_logprobs_noalloc. */
 #define DPO_NOALLOC_SCRATCH_BYTES (32u << 20)
 

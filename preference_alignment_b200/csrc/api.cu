@@ -478,6 +478,124 @@ dpo_status backward_core(const Plan& p, const dpo_batch* batch, const float* lse
   return DPO_OK;
 }
 
+// ---------------------------------------------------------------- token statistics
+// Positions a launch takes at most: the tiles' partials and lists of a chunk stay within a few
+// hundred MB, and 8,192 positions are enough tiles to fill the GPU's waves.
+constexpr int kStatsChunk = 8192;
+
+struct StatsPlan {
+  int chunk = 0;                       // positions per launch
+  size_t off_lp = 0, off_part = 0, off_tsum = 0, off_zy = 0, off_tau = 0, off_list = 0, total = 0;
+};
+
+// Layout behind `prefix` bytes for chunks of `chunk` positions, with room for n_lp log-probs.
+StatsPlan stats_layout(size_t prefix, long long n_lp, int V, bool bf16, int n_top, int chunk) {
+  StatsPlan s;
+  s.chunk = chunk;
+  const size_t ldp = align_up(chunk > 0 ? chunk : 1, 32);
+  const size_t tiles = stats_tiles(bf16, V);
+  size_t o = prefix;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, kAlign);
+    return at;
+  };
+  s.off_lp = take(sizeof(float) * static_cast<size_t>(n_lp));
+  s.off_part = take(sizeof(float2) * tiles * ldp);
+  s.off_tsum = take(sizeof(float) * tiles * ldp);
+  s.off_zy = take(sizeof(float) * ldp);
+  s.off_tau = take(sizeof(uint32_t) * ldp);
+  s.off_list = take(sizeof(float2) * tiles * ldp * stats_list_len(n_top));
+  s.total = o;
+  return s;
+}
+
+int stats_chunk_max(long long n) { return static_cast<int>(std::min<long long>(n, kStatsChunk)); }
+// The smallest chunk: one tile of token rows of a CTA pair, or of the SIMT route's.
+int stats_chunk_min(long long n, bool bf16) {
+  return static_cast<int>(std::min<long long>(n, bf16 ? 256 : 32));
+}
+
+// The largest chunk the workspace takes (total > ws_bytes: not even the smallest fits).
+StatsPlan stats_fit(size_t prefix, long long n_lp, long long n, int V, bool bf16, int n_top,
+                    size_t ws_bytes) {
+  const int step = bf16 ? 256 : 32;
+  int chunk = stats_chunk_max(n);
+  StatsPlan s = stats_layout(prefix, n_lp, V, bf16, n_top, chunk);
+  while (s.total > ws_bytes && chunk > stats_chunk_min(n, bf16)) {
+    chunk = (chunk - 1) / step * step;
+    s = stats_layout(prefix, n_lp, V, bf16, n_top, chunk);
+  }
+  return s;
+}
+
+dpo_status stats_out_ok(const dpo_token_stats_out* o) {
+  if (o == nullptr || o->n_top < 0 || o->n_top > DPO_MAX_TOP) return DPO_ERR_INVALID_ARG;
+  if (o->n_top > 0 && (o->top_ids == nullptr || o->top_logp == nullptr)) return DPO_ERR_INVALID_ARG;
+  return DPO_OK;
+}
+
+// Statistics of n positions in chunks: position i is row at[i] of H (at == NULL: i), rows
+// h_stride values apart; the bf16 route needs at == NULL (packed rows).
+dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, int V, int d,
+                      bool bf16, const void* H, const int* at, long long h_stride, const void* W,
+                      const int* y, const dpo_token_stats_out& o, float* logp, const DevInfo& di,
+                      cudaStream_t st) {
+  const DevCtl ctl = make_ctl(di);
+  for (long long i0 = 0; i0 < n; i0 += s.chunk) {
+    const int m = static_cast<int>(std::min<long long>(s.chunk, n - i0));
+    const int* yc = y != nullptr ? y + i0 : nullptr;
+    StatsBuf b;
+    b.part = reinterpret_cast<float2*>(w + s.off_part);
+    b.tsum = reinterpret_cast<float*>(w + s.off_tsum);
+    b.zy = reinterpret_cast<float*>(w + s.off_zy);
+    b.tau = reinterpret_cast<uint32_t*>(w + s.off_tau);
+    b.list = reinterpret_cast<float2*>(w + s.off_list);
+    b.ldp = static_cast<int>(align_up(s.chunk, 32));
+    if (bf16) {
+      CUtensorMap mA, mB;
+      if (!make_map(&mA, static_cast<const uint16_t*>(H) + i0 * h_stride, d, m, 2ull * h_stride,
+                    kBK, kBoxRows) ||
+          !make_map(&mB, W, d, V, 2ull * d, kBK, kBoxRows))
+        return DPO_ERR_CUDA;
+      if (launch_stats_bf16(mA, mB, b, o.n_top, m, V, d, yc, di.sms, sync, ctl, st) != cudaSuccess)
+        return DPO_ERR_CUDA;
+    } else {
+      const float* h = static_cast<const float*>(H) + (at != nullptr ? 0 : i0 * h_stride);
+      if (launch_stats_f32(h, at != nullptr ? at + i0 : nullptr, h_stride,
+                           static_cast<const float*>(W), b, o.n_top, m, V, d, yc, st) !=
+          cudaSuccess)
+        return DPO_ERR_CUDA;
+    }
+    if (launch_stats_finish(b, bf16, o.n_top, m, V, yc, logp ? logp + i0 : nullptr,
+                            o.entropy ? o.entropy + i0 : nullptr,
+                            o.lse_state ? o.lse_state + i0 : nullptr,
+                            o.n_top ? o.top_ids + i0 * o.n_top : nullptr,
+                            o.n_top ? o.top_logp + i0 * o.n_top : nullptr, ctl, st) != cudaSuccess)
+      return DPO_ERR_CUDA;
+  }
+  return DPO_OK;
+}
+
+// Host checks of a rows call (`sizes_only`: pointers are not looked at).
+dpo_status token_rows_ok(const dpo_token_rows* r, bool sizes_only) {
+  if (r == nullptr) return DPO_ERR_INVALID_ARG;
+  if (r->dtype == DPO_F16) return DPO_ERR_UNSUPPORTED;
+  if (r->dtype != DPO_BF16 && r->dtype != DPO_F32) return DPO_ERR_INVALID_ARG;
+  if (r->n < 0 || r->n > (1 << 30) || r->V < 1 || r->V > (1 << 24) || r->d < 1 || r->d > 65536)
+    return DPO_ERR_INVALID_ARG;
+  if (r->d % 8 != 0) return DPO_ERR_UNSUPPORTED;
+  if (sizes_only || r->n == 0) return DPO_OK;
+  // the bound keeps the row pitch within what a tensor map can hold
+  if (r->h_stride < r->d || r->h_stride > (1ll << 38)) return DPO_ERR_INVALID_ARG;
+  if (r->h_stride % 8 != 0) return DPO_ERR_UNSUPPORTED;
+  if (r->H == nullptr || r->W == nullptr || !aligned16(r->H) || !aligned16(r->W))
+    return DPO_ERR_INVALID_ARG;
+  return DPO_OK;
+}
+
+constexpr size_t kRowsPrefix = sizeof(int) * kSyncInts;   // the rows form's workspace prefix
+
 // Checks shared by the calls that continue from the dz a dpo_backward(dW = NULL) left
 // in the workspace: the whole batch in one chunk.
 dpo_status dz_resident(const Plan& p, const void* ws, size_t ws_bytes, int max_sms) {
@@ -490,6 +608,11 @@ dpo_status dz_resident(const Plan& p, const void* ws, size_t ws_bytes, int max_s
 }  // namespace
 
 int dpo::gemm_variant() { return g_gemm_variant.load(); }
+
+int dpo::device_sms() {
+  DevInfo di;
+  return device_info(&di) == DPO_OK ? di.sms : 0;
+}
 
 bool dpo::current_context(void** ctx) {
   // The runtime's calls above made the device's primary context current; the driver's
@@ -590,6 +713,78 @@ dpo_status dpo_shard_combine(const dpo_batch* batch, int32_t vocab_total, int32_
       cudaSuccess)
     return DPO_ERR_CUDA;
   return cuda_status(launch_rowsum(lp, sc.row_start, sc.prompt, p.R, p.L, seq_logp, tok_logp, st));
+}
+
+dpo_status dpo_token_stats_size(const dpo_batch* batch, int32_t n_top, size_t* bytes,
+                                size_t* min_bytes) {
+  Plan p;
+  const dpo_status s = make_plan(batch, &p);
+  if (s != DPO_OK) return s;
+  if (n_top < 0 || n_top > DPO_MAX_TOP) return DPO_ERR_INVALID_ARG;
+  const bool bf16 = p.dtype == DPO_BF16;
+  if (bytes) *bytes = stats_layout(p.prefix, p.Nc, p.V, bf16, n_top, stats_chunk_max(p.Nc)).total;
+  if (min_bytes)
+    *min_bytes = stats_layout(p.prefix, p.Nc, p.V, bf16, n_top, stats_chunk_min(p.Nc, bf16)).total;
+  return DPO_OK;
+}
+
+dpo_status dpo_token_stats(const dpo_batch* batch, const dpo_token_stats_out* out,
+                           float* seq_logp, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("dpo_token_stats");
+  Plan p;
+  dpo_status s = make_plan(batch, &p);
+  if (s != DPO_OK) return s;
+  if ((s = stats_out_ok(out)) != DPO_OK) return s;
+  const bool bf16 = p.dtype == DPO_BF16;
+  if (!ws_ok(ws, ws_bytes, 1)) return DPO_ERR_WORKSPACE;
+  const StatsPlan sp = stats_fit(p.prefix, p.Nc, p.Nc, p.V, bf16, out->n_top, ws_bytes);
+  if (sp.total > ws_bytes) return DPO_ERR_WORKSPACE;
+  DevInfo di;
+  if ((s = device_info(&di)) != DPO_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  if ((s = stage_schedule(p, batch, ws, make_ctl(di), st)) != DPO_OK) return s;
+  const Sched sc = sched_of(p, ws);
+  float* logp = out->logp;
+  if (logp == nullptr && seq_logp != nullptr) logp = reinterpret_cast<float*>(w + sp.off_lp);
+  s = stats_core(sp, w, sc.sync, p.Nc, p.V, p.d, bf16, bf16 ? w + p.off_hp : batch->H,
+                 bf16 ? nullptr : sc.dst, p.d, batch->W, sc.y, *out, logp, di, st);
+  if (s != DPO_OK || seq_logp == nullptr) return s;
+  return cuda_status(
+      launch_rowsum(logp, sc.row_start, sc.prompt, p.R, p.L, seq_logp, nullptr, st));
+}
+
+dpo_status dpo_token_stats_rows_size(const dpo_token_rows* rows, int32_t n_top, size_t* bytes,
+                                     size_t* min_bytes) {
+  const dpo_status s = token_rows_ok(rows, true);
+  if (s != DPO_OK) return s;
+  if (n_top < 0 || n_top > DPO_MAX_TOP) return DPO_ERR_INVALID_ARG;
+  const bool bf16 = rows->dtype == DPO_BF16;
+  const long long n = rows->n;
+  if (bytes)
+    *bytes = stats_layout(kRowsPrefix, 0, rows->V, bf16, n_top, stats_chunk_max(n)).total;
+  if (min_bytes)
+    *min_bytes = stats_layout(kRowsPrefix, 0, rows->V, bf16, n_top, stats_chunk_min(n, bf16)).total;
+  return DPO_OK;
+}
+
+dpo_status dpo_token_stats_rows(const dpo_token_rows* rows, const dpo_token_stats_out* out,
+                                void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("dpo_token_stats_rows");
+  dpo_status s = token_rows_ok(rows, false);
+  if (s != DPO_OK) return s;
+  if ((s = stats_out_ok(out)) != DPO_OK) return s;
+  if (out->logp != nullptr && rows->tokens == nullptr && rows->n > 0) return DPO_ERR_INVALID_ARG;
+  if (rows->n == 0) return DPO_OK;
+  const bool bf16 = rows->dtype == DPO_BF16;
+  if (!ws_ok(ws, ws_bytes, kRowsPrefix)) return DPO_ERR_WORKSPACE;
+  const StatsPlan sp = stats_fit(kRowsPrefix, 0, rows->n, rows->V, bf16, out->n_top, ws_bytes);
+  if (sp.total > ws_bytes) return DPO_ERR_WORKSPACE;
+  DevInfo di;
+  if ((s = device_info(&di)) != DPO_OK) return s;
+  return stats_core(sp, static_cast<uint8_t*>(ws), static_cast<int*>(ws), rows->n, rows->V, rows->d,
+                    bf16, rows->H, nullptr, rows->h_stride, rows->W, rows->tokens, *out, out->logp,
+                    di, static_cast<cudaStream_t>(stream));
 }
 
 dpo_status dpo_loss(int32_t B, int32_t layout, const float* pol, const float* ref, float beta,

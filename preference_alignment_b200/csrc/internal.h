@@ -139,6 +139,60 @@ cudaError_t launch_f32_dh(const float* G, const float* W, const Sched& s, int to
 cudaError_t launch_f32_dw(const float* G, const float* H, const Sched& s, int tok0, int Mc, int d,
                           int V, int v0, int v1, float* dW, int accumulate, cudaStream_t st);
 
+// Token statistics (log-prob of a given token, entropy, largest logits), see stats.cu.
+// Partials of a chunk of positions, in the workspace: S vocabulary tiles by ldp positions.
+struct StatsBuf {
+  float2* part;      // [S, ldp]
+  float* tsum;       // [S, ldp]
+  float* zy;         // [ldp]
+  uint32_t* tau;     // [ldp] (bf16)
+  float2* list;      // [S, stats_list_len, ldp]
+  int ldp;
+};
+int stats_list_len(int n_top);               // entries kept per tile for n_top alternatives
+int stats_tiles(bool bf16, int V);
+cudaError_t launch_stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const StatsBuf& b,
+                              int n_top, int n, int V, int d, const int* y, int sms, int* sync,
+                              const DevCtl& ctl, cudaStream_t st);
+// Row i of H is row at[i] (at == nullptr: i), h_stride values apart.
+cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, const float* W,
+                             const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
+                             cudaStream_t st);
+cudaError_t launch_stats_finish(const StatsBuf& b, bool bf16, int n_top, int n, int V, const int* y,
+                                float* logp, float* entropy, float* lse, int* top_ids,
+                                float* top_logp, const DevCtl& ctl, cudaStream_t st);
+
+// 8-bit activation checkpoints (checkpoint.cu) and the norm before the head (norm.cu).
+cudaError_t launch_ckpt_pack(bool bf16, int rows, int d, const void* x, long long stride,
+                             int8_t* codes, uint8_t* scales, cudaStream_t st);
+cudaError_t launch_ckpt_unpack(bool bf16, int rows, int d, const int8_t* codes,
+                               const uint8_t* scales, void* y, long long stride, cudaStream_t st);
+
+struct NormIn {
+  int rows, d, rms, bf16, wbf16;   // bf16: x, y, dx; wbf16: weight and bias
+  float eps;
+  const void* x;
+  long long x_stride;
+  const int8_t* codes;             // read x from a checkpoint (x is not read), or NULL
+  const uint8_t* scales;
+  const void *weight, *bias;
+};
+struct NormGradBuf {
+  const float *mean, *rstd;        // mean NULL: rms
+  const void* dy;
+  int dy_bf16;
+  long long dy_stride;
+  void* dx;
+  long long dx_stride;
+  float *dweight, *dbias;
+  int accumulate;
+  float* ws;                       // [2, kNormParts, d]
+};
+constexpr int kNormParts = 296;    // partial weight gradients at most: two blocks per SM
+cudaError_t launch_norm_fwd(const NormIn& n, void* y, long long y_stride, float* mean, float* rstd,
+                            int8_t* codes, uint8_t* scales, cudaStream_t st);
+cudaError_t launch_norm_bwd(const NormIn& n, const NormGradBuf& g, int sms, cudaStream_t st);
+
 // 64-bit order-independent fingerprint of a device buffer into out (device).
 cudaError_t launch_fingerprint(const void* data, unsigned long long bytes,
                                unsigned long long* out, int sms, cudaStream_t st);
@@ -149,6 +203,9 @@ cudaError_t launch_fingerprint(const void* data, unsigned long long bytes,
 // (clear: tiles claimed in raster order).
 enum GemmKind : int { kGemmForward = 0, kGemmGrad = 1, kGemmDH = 2, kGemmDW = 3 };
 int gemm_variant();
+
+// SMs of the current device (0 if the query failed).
+int device_sms();
 
 // The CUDA context current on this thread (false if none or the driver call failed).
 // Device addresses of the library's file-scope arrays are cached per context: a

@@ -460,3 +460,292 @@ def seq_logprobs_noalloc(batch: BatchArgs, want_grad: bool, seq_logp, tok_logp, 
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
+
+
+# ------------------------------------------------------------------ token statistics, norm, checkpoints
+MAX_TOP = 32                # DPO_MAX_TOP
+CHECKPOINT_BLOCK = 32       # DPO_CHECKPOINT_BLOCK
+NORM_KINDS = {"layer": 0, "rms": 1}
+
+_dtype_names = {}           # torch dtype -> its name, as _KINDS spells it
+
+
+def _kind_of(x):
+    """"bf16" or "f32" for a tensor of that element type, else a TypeError."""
+    name = _name_of(x)
+    for kind in ("bf16", "f32"):
+        if name in _KINDS[kind]:
+            return kind
+    raise TypeError(f"expected a bf16 or f32 tensor, got {name}")
+
+
+def _name_of(x):
+    name = _dtype_names.get(x.dtype)
+    if name is None:
+        name = _dtype_names[x.dtype] = str(x.dtype).replace("torch.", "")
+    return name
+
+
+def _on_device(x):
+    """The library works on the current device; a tensor elsewhere is refused."""
+    if not x.is_cuda:
+        raise ValueError(f"buffer of shape {tuple(x.shape)} is not in device memory")
+    import torch
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"buffer on {x.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
+def _buf(x, kind, n, what):
+    """Address of a dense device tensor of at least n elements of `kind`; None -> NULL, an
+    integer address as it is."""
+    if x is None or isinstance(x, int):
+        return x
+    _on_device(x)
+    if _name_of(x) not in _KINDS.get(kind, (kind,)):
+        raise TypeError(f"{what}: expected a {kind} buffer, got {_name_of(x)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{what}: buffer of shape {tuple(x.shape)} is not contiguous")
+    if x.numel() < n:
+        raise ValueError(f"{what}: {x.numel()} elements, {n} needed")
+    return x.data_ptr()
+
+
+def _row_view(x, what):
+    """(address, rows, d, stride) of a tensor of rows: 2-D with dense rows (any row stride), or
+    contiguous of any shape with its last dimension the row."""
+    _on_device(x)
+    shape = x.shape
+    if len(shape) == 2 and x.stride(1) == 1 and shape[1] > 0:
+        rows, d = shape
+        return x.data_ptr(), rows, d, (x.stride(0) if rows > 1 else d)
+    if len(shape) == 0 or shape[-1] < 1 or not x.is_contiguous():
+        raise ValueError(f"{what}: tensor of shape {tuple(shape)} has no dense rows")
+    d = shape[-1]
+    return x.data_ptr(), x.numel() // d, d, d
+
+
+_fns = {}
+
+
+def _fn(name, argtypes):
+    fn = _fns.get(name)
+    if fn is None:
+        fn = getattr(load(), name)
+        fn.argtypes = argtypes
+        fn.restype = ctypes.c_int
+        _fns[name] = fn
+    return fn
+
+
+_vp, _szp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
+
+
+class TokenStatsOut(ctypes.Structure):
+    _fields_ = [("logp", _vp), ("entropy", _vp), ("lse_state", _vp), ("n_top", ctypes.c_int32),
+                ("top_ids", _vp), ("top_logp", _vp)]
+
+
+class TokenRows(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("d", ctypes.c_int32), ("V", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("H", _vp), ("h_stride", ctypes.c_int64), ("W", _vp),
+                ("tokens", _vp)]
+
+
+def _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp):
+    n_top = int(n_top)
+    return TokenStatsOut(_buf(logp, "f32", n, "logp"), _buf(entropy, "f32", n, "entropy"),
+                         _buf(lse_state, "f32", n, "lse_state"), n_top,
+                         _buf(top_ids, "i32", n * n_top, "top_ids"),
+                         _buf(top_logp, "f32", n * n_top, "top_logp"))
+
+
+def token_stats_size(batch: BatchArgs, n_top: int):
+    """(bytes, min_bytes) of token_stats' workspace."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    fn = _fn("dpo_token_stats_size", [ctypes.POINTER(Batch), ctypes.c_int32, _szp, _szp])
+    _check(fn(ctypes.byref(batch.c), int(n_top), ctypes.byref(a), ctypes.byref(b)),
+           "dpo_token_stats_size")
+    return a.value, b.value
+
+
+def token_stats(batch: BatchArgs, n_top: int, ws, logp=None, entropy=None, lse_state=None,
+                seq_logp=None, top_ids=None, top_logp=None, ws_bytes=None, stream=None):
+    """dpo_token_stats: per scored position (row order) the target's log-prob, the entropy, the
+    log-sum-exp that backward() reads and the n_top largest logits' ids and log-probs; per row
+    the sum of the log-probs. Outputs left out are not written."""
+    out = _stats_out(batch.n_scored, n_top, logp, entropy, lse_state, top_ids, top_logp)
+    fn = _fn("dpo_token_stats", [ctypes.POINTER(Batch), ctypes.POINTER(TokenStatsOut), _vp, _vp,
+                                 ctypes.c_size_t, _vp])
+    _check(fn(ctypes.byref(batch.c), ctypes.byref(out), _buf(seq_logp, "f32", batch.c.R, "seq_logp"),
+              _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)), "dpo_token_stats")
+
+
+def token_stats_rows_size(n: int, d: int, V: int, n_top: int, dtype="bf16"):
+    """(bytes, min_bytes) of token_stats_rows' workspace."""
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    rows = TokenRows(int(n), int(d), int(V), DTYPES[dtype] if isinstance(dtype, str) else int(dtype),
+                     None, int(d), None, None)
+    fn = _fn("dpo_token_stats_rows_size",
+             [ctypes.POINTER(TokenRows), ctypes.c_int32, _szp, _szp])
+    _check(fn(ctypes.byref(rows), int(n_top), ctypes.byref(a), ctypes.byref(b)),
+           "dpo_token_stats_rows_size")
+    return a.value, b.value
+
+
+def token_stats_rows(H, W, tokens, n_top: int, ws, logp=None, entropy=None, lse_state=None,
+                     top_ids=None, top_logp=None, ws_bytes=None, stream=None):
+    """dpo_token_stats_rows: token_stats for independent hidden rows, H [n, d] (any row stride)
+    against W [V, d], tokens int32 [n] or None (then logp is None too)."""
+    h, n, d, stride = _row_view(H, "H")
+    if len(W.shape) != 2 or W.shape[1] != d:
+        raise ValueError(f"W of shape {tuple(W.shape)} does not fit rows of {d}")
+    kind = _kind_of(H)
+    rows = TokenRows(n, d, W.shape[0], DTYPES[kind], h, stride, _buf(W, kind, 0, "W"),
+                     _buf(tokens, "i32", n, "tokens"))
+    out = _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp)
+    fn = _fn("dpo_token_stats_rows", [ctypes.POINTER(TokenRows), ctypes.POINTER(TokenStatsOut), _vp,
+                                      ctypes.c_size_t, _vp])
+    _check(fn(ctypes.byref(rows), ctypes.byref(out), _ptr(ws), _nbytes(ws, ws_bytes),
+              _stream(stream)), "dpo_token_stats_rows")
+
+
+class CheckpointC(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp)]
+
+
+class Checkpoint:
+    """Activations held in 8 bits: codes int8 [rows, d] and scales uint8 [rows, ceil(d / 32)],
+    device tensors (Checkpoint.empty makes them)."""
+
+    def __init__(self, codes, scales):
+        if len(codes.shape) != 2:
+            raise ValueError("codes must be [rows, d]")
+        self.codes, self.scales = codes, scales
+        self.rows, self.d = codes.shape
+        blocks = -(-self.d // CHECKPOINT_BLOCK)
+        if tuple(scales.shape) != (self.rows, blocks):
+            raise ValueError(f"scales must be [{self.rows}, {blocks}], got {tuple(scales.shape)}")
+
+    @classmethod
+    def empty(cls, rows: int, d: int, device="cuda"):
+        import torch
+        return cls(torch.empty(rows, d, dtype=torch.int8, device=device),
+                   torch.empty(rows, -(-d // CHECKPOINT_BLOCK), dtype=torch.uint8, device=device))
+
+    def _c(self):
+        return CheckpointC(_buf(self.codes, "int8", self.rows * self.d, "codes"),
+                           _buf(self.scales, "uint8", 0, "scales"))
+
+
+def _fits(rows, d, what, rows2, d2):
+    if (rows, d) != (rows2, d2):
+        raise ValueError(f"{what} is {rows2} x {d2}, expected {rows} x {d}")
+
+
+def checkpoint_pack(x, out: Checkpoint, stream=None):
+    """dpo_checkpoint_pack: hold the rows of x (bf16 or f32, any row stride) in out."""
+    p, rows, d, stride = _row_view(x, "x")
+    _fits(rows, d, "out", out.rows, out.d)
+    c = out._c()
+    fn = _fn("dpo_checkpoint_pack", [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp,
+                                     ctypes.c_int64, ctypes.POINTER(CheckpointC), _vp])
+    _check(fn(DTYPES[_kind_of(x)], rows, d, p, stride, ctypes.byref(c), _stream(stream)),
+           "dpo_checkpoint_pack")
+
+
+def checkpoint_unpack(held: Checkpoint, y, stream=None):
+    """dpo_checkpoint_unpack: the values held, into the rows of y (bf16 or f32)."""
+    p, rows, d, stride = _row_view(y, "y")
+    _fits(held.rows, held.d, "y", rows, d)
+    c = held._c()
+    fn = _fn("dpo_checkpoint_unpack", [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                       ctypes.POINTER(CheckpointC), _vp, ctypes.c_int64, _vp])
+    _check(fn(DTYPES[_kind_of(y)], rows, d, ctypes.byref(c), p, stride, _stream(stream)),
+           "dpo_checkpoint_unpack")
+
+
+class NormC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", _vp), ("x_stride", ctypes.c_int64),
+                ("from_", ctypes.POINTER(CheckpointC)), ("weight", _vp), ("bias", _vp)]
+
+
+class NormGradsC(ctypes.Structure):
+    _fields_ = [("mean", _vp), ("rstd", _vp), ("dy", _vp), ("dy_dtype", ctypes.c_int32),
+                ("dy_stride", ctypes.c_int64), ("dx", _vp), ("dx_stride", ctypes.c_int64),
+                ("dweight", _vp), ("dbias", _vp), ("accumulate", ctypes.c_int32)]
+
+
+def _norm(x, kind_out, weight, bias, kind, eps):
+    """(NormC, rows, d) of a norm of x, a tensor of rows or a Checkpoint (then kind_out is the
+    other side's element type)."""
+    if isinstance(x, Checkpoint):
+        p, rows, d, stride = None, x.rows, x.d, 0
+        held = ctypes.pointer(x._c())
+    else:
+        p, rows, d, stride = _row_view(x, "x")
+        held = None
+        kind_out = _kind_of(x)
+    wkind = _kind_of(weight) if weight is not None else "f32"
+    if bias is not None:
+        bkind = _kind_of(bias)
+        if weight is not None and bkind != wkind:
+            raise TypeError(f"weight is {wkind}, bias {bkind}")
+        wkind = bkind
+    n = NormC(NORM_KINDS[kind] if isinstance(kind, str) else int(kind), DTYPES[kind_out],
+              DTYPES[wkind], rows, d, float(eps), p, stride, held,
+              _buf(weight, wkind, d, "weight"), _buf(bias, wkind, d, "bias"))
+    return n, rows, d
+
+
+def norm_forward(x, y, weight=None, bias=None, kind="layer", eps=1e-5, mean=None, rstd=None,
+                 save: Optional[Checkpoint] = None, stream=None):
+    """dpo_norm_forward: y = norm(x) by rows, kind "layer" or "rms"; mean and rstd (f32 [rows])
+    are what norm_backward reads; save also holds x in 8 bits. x may be a Checkpoint: the norm
+    of the values it holds."""
+    n, rows, d = _norm(x, _kind_of(y), weight, bias, kind, eps)
+    p, yr, yd, stride = _row_view(y, "y")
+    _fits(rows, d, "y", yr, yd)
+    if DTYPES[_kind_of(y)] != n.dtype:
+        raise TypeError("y must have x's element type")
+    c = None
+    if save is not None:
+        _fits(rows, d, "save", save.rows, save.d)
+        c = ctypes.byref(save._c())
+    fn = _fn("dpo_norm_forward", [ctypes.POINTER(NormC), _vp, ctypes.c_int64, _vp, _vp,
+                                  ctypes.POINTER(CheckpointC), _vp])
+    _check(fn(ctypes.byref(n), p, stride, _buf(mean, "f32", rows, "mean"),
+              _buf(rstd, "f32", rows, "rstd"), c, _stream(stream)), "dpo_norm_forward")
+
+
+def norm_workspace_size(rows: int, d: int) -> int:
+    """Workspace bytes of norm_backward."""
+    b = ctypes.c_size_t()
+    fn = _fn("dpo_norm_workspace_size", [ctypes.c_int32, ctypes.c_int32, _szp])
+    _check(fn(int(rows), int(d), ctypes.byref(b)), "dpo_norm_workspace_size")
+    return b.value
+
+
+def norm_backward(x, dy, mean, rstd, dx=None, weight=None, dweight=None, dbias=None, kind="layer",
+                  accumulate=False, ws=None, ws_bytes=None, stream=None):
+    """dpo_norm_backward: dx (x's element type; for a Checkpoint, its own), and the fp32 weight
+    and bias gradients, from the forward's x (a tensor of rows or the Checkpoint that held it),
+    its statistics and dy (bf16 or f32 rows)."""
+    n, rows, d = _norm(x, _kind_of(dx) if dx is not None else "bf16", weight, None, kind, 0.0)
+    p, yr, yd, stride = _row_view(dy, "dy")
+    _fits(rows, d, "dy", yr, yd)
+    q, dx_stride = None, d
+    if dx is not None:
+        q, xr, xd, dx_stride = _row_view(dx, "dx")
+        _fits(rows, d, "dx", xr, xd)
+        if DTYPES[_kind_of(dx)] != n.dtype:
+            raise TypeError("dx must have x's element type")
+    g = NormGradsC(_buf(mean, "f32", rows, "mean"), _buf(rstd, "f32", rows, "rstd"), p,
+                   DTYPES[_kind_of(dy)], stride, q, dx_stride, _buf(dweight, "f32", d, "dweight"),
+                   _buf(dbias, "f32", d, "dbias"), 1 if accumulate else 0)
+    fn = _fn("dpo_norm_backward", [ctypes.POINTER(NormC), ctypes.POINTER(NormGradsC), _vp,
+                                   ctypes.c_size_t, _vp])
+    _check(fn(ctypes.byref(n), ctypes.byref(g), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
+           "dpo_norm_backward")
