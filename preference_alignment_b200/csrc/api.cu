@@ -485,15 +485,21 @@ constexpr int kStatsChunk = 8192;
 
 struct StatsPlan {
   int chunk = 0;                       // positions per launch
+  int ldp = 0;                         // positions a row of partials has room for
   size_t off_lp = 0, off_part = 0, off_tsum = 0, off_zy = 0, off_tau = 0, off_list = 0, total = 0;
 };
 
-// Layout behind `prefix` bytes for chunks of `chunk` positions, with room for n_lp log-probs.
-StatsPlan stats_layout(size_t prefix, long long n_lp, int V, bool bf16, int n_top, int chunk) {
+// Layout behind `prefix` bytes for n positions in chunks of `chunk`, with room for n_lp log-probs.
+StatsPlan stats_layout(size_t prefix, long long n_lp, long long n, int V, bool bf16, int n_top,
+                       int chunk) {
   StatsPlan s;
   s.chunk = chunk;
-  const size_t ldp = align_up(chunk > 0 ? chunk : 1, 32);
-  const size_t tiles = stats_tiles(bf16, V);
+  const size_t ctas = stats_stream_ctas(V, kStreamCtas);
+  const bool stream = bf16 && n <= kStreamMax;
+  const size_t tiles = stream ? ctas : stats_tiles(bf16, V);
+  const size_t lists = stream ? ctas * kStreamLists : tiles;
+  const size_t ldp = stream ? n : align_up(chunk > 0 ? chunk : 1, 32);
+  s.ldp = static_cast<int>(ldp);
   size_t o = prefix;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -504,8 +510,8 @@ StatsPlan stats_layout(size_t prefix, long long n_lp, int V, bool bf16, int n_to
   s.off_part = take(sizeof(float2) * tiles * ldp);
   s.off_tsum = take(sizeof(float) * tiles * ldp);
   s.off_zy = take(sizeof(float) * ldp);
-  s.off_tau = take(sizeof(uint32_t) * ldp);
-  s.off_list = take(sizeof(float2) * tiles * ldp * stats_list_len(n_top));
+  s.off_tau = take(sizeof(uint32_t) * ldp * stats_list_len(n_top));
+  s.off_list = take(sizeof(float2) * lists * ldp * stats_list_len(n_top));
   s.total = o;
   return s;
 }
@@ -521,10 +527,10 @@ StatsPlan stats_fit(size_t prefix, long long n_lp, long long n, int V, bool bf16
                     size_t ws_bytes) {
   const int step = bf16 ? 256 : 32;
   int chunk = stats_chunk_max(n);
-  StatsPlan s = stats_layout(prefix, n_lp, V, bf16, n_top, chunk);
+  StatsPlan s = stats_layout(prefix, n_lp, n, V, bf16, n_top, chunk);
   while (s.total > ws_bytes && chunk > stats_chunk_min(n, bf16)) {
     chunk = (chunk - 1) / step * step;
-    s = stats_layout(prefix, n_lp, V, bf16, n_top, chunk);
+    s = stats_layout(prefix, n_lp, n, V, bf16, n_top, chunk);
   }
   return s;
 }
@@ -551,8 +557,20 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
     b.zy = reinterpret_cast<float*>(w + s.off_zy);
     b.tau = reinterpret_cast<uint32_t*>(w + s.off_tau);
     b.list = reinterpret_cast<float2*>(w + s.off_list);
-    b.ldp = static_cast<int>(align_up(s.chunk, 32));
-    if (bf16) {
+    b.ldp = s.ldp;
+    int S = stats_tiles(bf16, V);
+    const bool stream = bf16 && n <= kStreamMax;   // by the call's n: a chunk never changes the route
+    if (stream) {
+      CUtensorMap mW, mWp, mH;
+      if (!make_map(&mW, W, d, V, 2ull * d, kBK, kStreamRows) ||
+          !make_map(&mWp, W, d, V, 2ull * d, kBK, stats_stream_share(V, di.sms)) ||
+          !make_map(&mH, H, d, m, 2ull * h_stride, kBK, stats_stream_cols(m)))
+        return DPO_ERR_CUDA;
+      S = stats_stream_ctas(V, std::min(di.sms, kStreamCtas));
+      if (launch_stats_stream(mW, mWp, mH, b, o.n_top, m, V, d, yc, di.sms, ctl, st) !=
+          cudaSuccess)
+        return DPO_ERR_CUDA;
+    } else if (bf16) {
       CUtensorMap mA, mB;
       if (!make_map(&mA, static_cast<const uint16_t*>(H) + i0 * h_stride, d, m, 2ull * h_stride,
                     kBK, kBoxRows) ||
@@ -567,7 +585,7 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
           cudaSuccess)
         return DPO_ERR_CUDA;
     }
-    if (launch_stats_finish(b, bf16, o.n_top, m, V, yc, logp ? logp + i0 : nullptr,
+    if (launch_stats_finish(b, bf16, S, stream, o.n_top, m, V, yc, logp ? logp + i0 : nullptr,
                             o.entropy ? o.entropy + i0 : nullptr,
                             o.lse_state ? o.lse_state + i0 : nullptr,
                             o.n_top ? o.top_ids + i0 * o.n_top : nullptr,
@@ -722,9 +740,9 @@ dpo_status dpo_token_stats_size(const dpo_batch* batch, int32_t n_top, size_t* b
   if (s != DPO_OK) return s;
   if (n_top < 0 || n_top > DPO_MAX_TOP) return DPO_ERR_INVALID_ARG;
   const bool bf16 = p.dtype == DPO_BF16;
-  if (bytes) *bytes = stats_layout(p.prefix, p.Nc, p.V, bf16, n_top, stats_chunk_max(p.Nc)).total;
+  if (bytes) *bytes = stats_layout(p.prefix, p.Nc, p.Nc, p.V, bf16, n_top, stats_chunk_max(p.Nc)).total;
   if (min_bytes)
-    *min_bytes = stats_layout(p.prefix, p.Nc, p.V, bf16, n_top, stats_chunk_min(p.Nc, bf16)).total;
+    *min_bytes = stats_layout(p.prefix, p.Nc, p.Nc, p.V, bf16, n_top, stats_chunk_min(p.Nc, bf16)).total;
   return DPO_OK;
 }
 
@@ -762,9 +780,9 @@ dpo_status dpo_token_stats_rows_size(const dpo_token_rows* rows, int32_t n_top, 
   const bool bf16 = rows->dtype == DPO_BF16;
   const long long n = rows->n;
   if (bytes)
-    *bytes = stats_layout(kRowsPrefix, 0, rows->V, bf16, n_top, stats_chunk_max(n)).total;
+    *bytes = stats_layout(kRowsPrefix, 0, n, rows->V, bf16, n_top, stats_chunk_max(n)).total;
   if (min_bytes)
-    *min_bytes = stats_layout(kRowsPrefix, 0, rows->V, bf16, n_top, stats_chunk_min(n, bf16)).total;
+    *min_bytes = stats_layout(kRowsPrefix, 0, n, rows->V, bf16, n_top, stats_chunk_min(n, bf16)).total;
   return DPO_OK;
 }
 

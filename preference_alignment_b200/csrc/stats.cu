@@ -13,23 +13,9 @@
 
 #include "internal.h"
 #include "gemm_launch.cuh"
+#include "stats.cuh"
 
 namespace dpo {
-
-constexpr float kLog2eS = 1.4426950408889634f;
-constexpr float kLn2S = 0.6931471805599453f;
-// Logits at or below this count as -inf: they add nothing and are no alternative.
-constexpr float kFloor = -1e30f;
-
-// Order-preserving map of floats to unsigned integers; 0 is below every float's image.
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);           // -0 counts as 0
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-__device__ __forceinline__ float from_ordered(uint32_t o) {
-  if (o == 0) return -INFINITY;
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
-}
 
 // x[j] with j known only at run time: five rounds of selects, so x stays in registers.
 __device__ __forceinline__ float pick32(const float (&x)[32], int j) {
@@ -46,11 +32,14 @@ __device__ __forceinline__ float pick32(const float (&x)[32], int j) {
 }
 
 // Per-tile lists of the K largest logits: a list is worth writing only if it can still
-// matter. Each position has a threshold in global memory, the largest K-th value any of its
-// finished tiles has published (atomicMax; the maximum does not depend on the order), a lower
-// bound of the position's K-th largest logit. A tile takes a logit only if it reaches the
-// threshold, and the finish reads a tile's list only if the tile's maximum reaches the final
-// threshold: such a tile did write it, because the threshold it saw was no higher.
+// matter. The tiles fall into K groups (tile mod K); each position has a threshold per group in
+// global memory, the largest logit any finished tile of the group has bid (atomicMax; the maximum
+// does not depend on the order). K groups stand for K different logits, so the smallest of them is
+// a lower bound of the position's K-th largest logit, and a close one: about K log K logits reach
+// it. A tile takes a logit only if it reaches the bound, and the finish looks at a tile only if
+// the tile's maximum reaches the final bound: such a tile did write its list, because the bound it
+// saw was no higher. (With the largest K-th logit of any one tile as the bound, 4 logits of every
+// tile reached it at K = 8.)
 template <int K>
 struct EpiStats {
   static constexpr bool kStaging = false;
@@ -60,7 +49,7 @@ struct EpiStats {
     float2* part;        // [S, ldp] (m, S)
     float* tsum;         // [S, ldp] T
     float* zy;           // [ldp] target logit
-    uint32_t* tau;       // [ldp] thresholds, zeroed before the launch
+    uint32_t* tau;       // [K, ldp] thresholds, zeroed before the launch
     float2* list;        // [S, K, ldp] (logit, id), falling, fillers (<= kFloor, -)
     int n, V, ldp;
   };
@@ -70,6 +59,7 @@ struct EpiStats {
   float mx, ref, s, t, zyv, tauv;
   float val[kList];
   int id[kList];
+  uint32_t bid;          // the highest bid of this tile's group so far
 
   __device__ __forceinline__ void begin(const Params& p, int m_row, int nt_, int, const EpiCtx&) {
     nt = nt_;
@@ -85,26 +75,20 @@ struct EpiStats {
     t = 0.f;
     zyv = 0.f;
     if (K > 0) {
-      tauv = valid ? from_ordered(__ldcg(p.tau + tok)) : INFINITY;   // padding rows take nothing
+      uint32_t th = 0xffffffffu;
+      bid = 0;
+#pragma unroll
+      for (int g = 0; g < kList; ++g) {
+        const uint32_t o = valid ? __ldcg(p.tau + static_cast<long long>(g) * p.ldp + tok) : 0u;
+        th = min(th, o);
+        if (g == nt % kList) bid = o;
+      }
+      tauv = valid ? from_ordered(th) : INFINITY;                // padding rows take nothing
 #pragma unroll
       for (int j = 0; j < kList; ++j) {
         val[j] = kFloor;
         id[j] = 0;
       }
-    }
-  }
-
-  // Sorted insert; among equal logits the earlier column stays in front.
-  __device__ __forceinline__ void insert(float x, int col) {
-#pragma unroll
-    for (int j = kList - 1; j > 0; --j) {
-      const bool here = x > val[j], above = x > val[j - 1];
-      id[j] = above ? id[j - 1] : (here ? col : id[j]);
-      val[j] = above ? val[j - 1] : (here ? x : val[j]);
-    }
-    if (x > val[0]) {
-      val[0] = x;
-      id[0] = col;
     }
   }
 
@@ -121,7 +105,8 @@ struct EpiStats {
 #pragma unroll
     for (int j = 1; j < 32; ++j) cm = fmaxf(cm, x[j]);
     const float nm = fmaxf(mx, cm);
-    const float nref = nm * kLog2eS;                 // the sums' reference, in powers of two
+    // the sums' reference in powers of two: the rounded product, not a fused one
+    const float nref = __fmul_rn(nm, kLog2eS);
     const float back = ref - nref;                   // <= 0; exactly 0 while the maximum stands
     const float f = ex2_approx(back);
     t = f * fmaf(s, back, t);
@@ -151,7 +136,7 @@ struct EpiStats {
         while (__any_sync(0xffffffffu, m != 0)) {
           const int j = m ? __ffs(m) - 1 : 0;
           const float xv = pick32(x, j);
-          if (m != 0) insert(xv, c * 32 + j);
+          if (m != 0) insert_sorted<kList>(val, id, xv, c * 32 + j);
           m &= m - 1;
         }
       }
@@ -171,34 +156,11 @@ struct EpiStats {
 #pragma unroll
       for (int j = 0; j < kList; ++j)
         l[static_cast<long long>(j) * p.ldp] = make_float2(val[j], __int_as_float(nt * kBN + id[j]));
-      if (val[kList - 1] > fmaxf(tauv, kFloor)) atomicMax(p.tau + tok, ordered(val[kList - 1]));
+      if (ordered(val[0]) > bid)
+        atomicMax(p.tau + static_cast<long long>(nt % kList) * p.ldp + tok, ordered(val[0]));
     }
   }
 };
-
-// ------------------------------------------------------------------ lists across a warp
-// A falling list of 32 (logit, id) entries, entry j in lane j.
-struct Entry {
-  float v;
-  int id;
-};
-
-__device__ __forceinline__ bool ahead(const Entry& a, const Entry& b) {
-  return a.v > b.v || (a.v == b.v && a.id < b.id);
-}
-
-// The 32 best of two falling lists: entry j against entry 31 - j of the other leaves the best
-// 32 in an order that falls and then rises (or the reverse), which five exchange rounds sort.
-__device__ __forceinline__ void merge_lists(Entry& a, Entry b, int lane) {
-  b.v = __shfl_sync(0xffffffffu, b.v, 31 - lane);
-  b.id = __shfl_sync(0xffffffffu, b.id, 31 - lane);
-  if (ahead(b, a)) a = b;
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    const Entry o{__shfl_xor_sync(0xffffffffu, a.v, w), __shfl_xor_sync(0xffffffffu, a.id, w)};
-    if (((lane & w) == 0) == ahead(o, a)) a = o;
-  }
-}
 
 // ------------------------------------------------------------------ finish
 struct StatsOut {
@@ -207,48 +169,49 @@ struct StatsOut {
   int n_top;
 };
 
-// One warp per position. Lane l joins tiles l, l + 32, ... (S and T in fp64, so that a
-// vocabulary of millions loses nothing), then the lanes join by a fixed tree; tiles whose
-// maximum reaches the threshold bring their lists in, in rising tile order.
-template <int K>
+// WPP warps per position (the block's 8 warps hold 8 / WPP positions): lane l of warp w joins
+// tiles 32 w + l, 32 w + l + 32 WPP, ..., then lanes and warps join in a fixed order.
+//
+// Alternatives. The K largest logits lie in the K first tiles by (maximum falling, id rising): a
+// logit of any other tile has the maxima of those K ahead of it. So the warp keeps the K first
+// tiles while it reads the partials; their maxima are then a sorted list of logits already, and
+// the tiles' second, third, ... entries go in until none is ahead of the list's last. (Joining
+// every tile's list instead, in one chain of dependent loads, took 230 us of the 435 us of a
+// single token at V = 128,256.)
+//
+// stream false: S tiles in id order, each with a sum and (if its maximum reaches the threshold) a list.
+// stream true: the streaming form, S CTAs with a sum each and segs lists each, whose first entries
+// tell their order.
+template <int K, int WPP>
 __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__ part,
                                                       const float* __restrict__ tsum,
                                                       const float2* __restrict__ list,
                                                       const uint32_t* __restrict__ tau,
                                                       const float* __restrict__ zy,
                                                       const int* __restrict__ y, int n, int S,
-                                                      int V, int ldp, StatsOut out, DevCtl ctl) {
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= n) return;
-  float M = -INFINITY;
-  double s = 0.0, t = 0.0;
-  Entry best{-INFINITY, -1};
-  const float tauv = K > 0 && tau != nullptr ? from_ordered(__ldg(tau + i)) : -INFINITY;
-  auto join = [&](float m, double s2, double t2) {
-    if (m == -INFINITY) return;
-    if (m > M) {
-      if (M != -INFINITY) {
-        const double f = expf(M - m), back = M - m;
-        t = f * (t + s * back) + t2;
-        s = f * s + s2;
-      } else {
-        s = s2;
-        t = t2;
-      }
-      M = m;
-    } else {
-      const double f = expf(m - M), back = m - M;
-      t += f * (t2 + s2 * back);
-      s += f * s2;
-    }
-  };
-  for (int base = 0; base < S; base += 128) {
-    float2 q[4];
-    float tq[4];
+                                                      int V, int ldp, bool stream, StatsOut out, DevCtl ctl) {
+  constexpr int kJoin = WPP > 1 ? WPP : 1;
+  __shared__ float sm[kJoin];
+  __shared__ double ss[kJoin], st[kJoin];
+  __shared__ float bv[kJoin][32];
+  __shared__ int bi[kJoin][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i = WPP > 1 ? blockIdx.x : blockIdx.x * 8 + warp;
+  const int w = WPP > 1 ? warp : 0;
+  if (i >= n) return;                     // whole warps; whole blocks when WPP > 1
+  Sums a;
+  Entry best{-INFINITY, -1};              // tiles by their maximum
+  float tauv = -INFINITY;
+  if (K > 0 && tau != nullptr)
+    tauv = from_ordered(__reduce_min_sync(
+        0xffffffffu, lane < K ? __ldg(tau + static_cast<long long>(lane) * ldp + i) : 0xffffffffu));
+  constexpr int U = 4;
+  for (int base = 0; base < S; base += 32 * WPP * U) {
+    float2 q[U];
+    float tq[U];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = base + u * 32 + lane;
+    for (int u = 0; u < U; ++u) {
+      const int k = base + (u * WPP + w) * 32 + lane;
       q[u] = make_float2(-INFINITY, 0.f);
       tq[u] = 0.f;
       if (k < S) {
@@ -257,53 +220,105 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) join(q[u].x, q[u].y, tq[u]);
-    if (K > 0) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t hit = __ballot_sync(0xffffffffu, q[u].x > kFloor && q[u].x >= tauv);
+    for (int u = 0; u < U; ++u) {
+      a.join(q[u].x, q[u].y, tq[u]);
+      if (K > 0 && !stream) {
+        // tiles come in rising order: an equal maximum is behind the ones held
+        const float m = q[u].x > kFloor && q[u].x >= tauv ? q[u].x : -INFINITY;
+        uint32_t hit = __ballot_sync(0xffffffffu, m > __shfl_sync(0xffffffffu, best.v, K - 1));
         while (hit) {
-          const int k = base + u * 32 + __ffs(hit) - 1;
+          const int src = __ffs(hit) - 1;
+          insert_entry(best, Entry{__shfl_sync(0xffffffffu, m, src),
+                                   base + (u * WPP + w) * 32 + src}, lane);
           hit &= hit - 1;
-          Entry e{-INFINITY, -1};
-          if (lane < K) {
-            const float2 r = __ldg(list + (static_cast<long long>(k) * K + lane) * ldp + i);
-            if (r.x > kFloor) e = Entry{r.x, __float_as_int(r.y)};
-          }
-          // a later tile's equal logit has the higher id: only a larger one can enter a full list
-          const float first = __shfl_sync(0xffffffffu, e.v, 0);
-          const float last = __shfl_sync(0xffffffffu, best.v, K - 1);
-          if (first > last) merge_lists(best, e, lane);
+          hit &= __ballot_sync(0xffffffffu, m > __shfl_sync(0xffffffffu, best.v, K - 1));
         }
       }
     }
   }
+  if (K > 0 && stream) {
+    const int sets = S * kSSegs;
+    for (int base = 0; base < sets; base += 32 * WPP * U) {
+      Entry e[U];
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    const float m2 = __shfl_down_sync(0xffffffffu, M, w);
-    const double s2 = __shfl_down_sync(0xffffffffu, s, w);
-    const double t2 = __shfl_down_sync(0xffffffffu, t, w);
-    join(m2, s2, t2);
+      for (int u = 0; u < U; ++u) {
+        const int k = base + (u * WPP + w) * 32 + lane;
+        e[u] = Entry{-INFINITY, -1};
+        if (k < sets) {
+          const float2 r = __ldg(list + static_cast<long long>(k) * K * ldp + i);
+          if (r.x > kFloor && r.x >= tauv) e[u] = Entry{r.x, __float_as_int(r.y)};
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) take_entries<K>(best, e[u], lane);
+    }
   }
-  const double ls = log(s);
-  const float lse = static_cast<float>(M + ls);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_down_sync(0xffffffffu, a.M, o);
+    const double s2 = __shfl_down_sync(0xffffffffu, a.s, o);
+    const double t2 = __shfl_down_sync(0xffffffffu, a.t, o);
+    a.join(m2, s2, t2);
+  }
+  if (WPP > 1) {
+    if (lane == 0) {
+      sm[w] = a.M;
+      ss[w] = a.s;
+      st[w] = a.t;
+    }
+    if (K > 0) {
+      bv[w][lane] = best.v;
+      bi[w][lane] = best.id;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    if (lane == 0)
+      for (int k = 1; k < WPP; ++k) a.join(sm[k], ss[k], st[k]);
+    if (K > 0)
+      for (int k = 1; k < WPP; ++k) merge_lists(best, Entry{bv[k][lane], bi[k][lane]}, lane);
+  }
+  const double ls = log(a.s);
   if (lane == 0) {
-    if (out.lse != nullptr) out.lse[i] = lse;
-    if (out.entropy != nullptr) out.entropy[i] = static_cast<float>(ls - t / s);
+    if (out.lse != nullptr) out.lse[i] = static_cast<float>(a.M + ls);
+    if (out.entropy != nullptr) out.entropy[i] = static_cast<float>(ls - a.t / a.s);
     if (y != nullptr) {
       const int yi = __ldg(y + i);
       const bool ok = yi >= 0 && yi < V;
       if (!ok) record_status(ctl, kStatusBadTarget);
       // against M before log S: z_y - lse would round away what large logits leave
       if (out.logp != nullptr)
-        out.logp[i] = ok ? static_cast<float>((static_cast<double>(__ldg(zy + i)) - M) - ls) : 0.f;
+        out.logp[i] = ok ? static_cast<float>((static_cast<double>(__ldg(zy + i)) - a.M) - ls) : 0.f;
     }
   }
-  const double m0 = __shfl_sync(0xffffffffu, M, 0), l0 = __shfl_sync(0xffffffffu, ls, 0);
-  if (K > 0 && lane < out.n_top) {
-    const long long at = static_cast<long long>(i) * out.n_top + lane;
-    out.top_ids[at] = best.id;
-    out.top_logp[at] = best.id >= 0 ? static_cast<float>((best.v - m0) - l0) : -INFINITY;
+  if (K > 0) {
+    const double m0 = __shfl_sync(0xffffffffu, a.M, 0), l0 = __shfl_sync(0xffffffffu, ls, 0);
+    bool more = lane < K && best.id >= 0;
+    int tile = best.id;                   // lane j: the j-th tile
+    if (stream && more) {
+      int cta, row;
+      StreamSplit(V, S).owner(best.id, cta, row);
+      tile = cta * kSSegs + row / kSegRows;
+    }
+    const float2* mine = list + static_cast<long long>(tile) * K * ldp + i;
+    Entry top{-INFINITY, -1};
+    if (more) {
+      const float2 r = __ldg(mine);
+      top = Entry{r.x, __float_as_int(r.y)};
+    }
+    for (int j = 1; j < K; ++j) {
+      Entry e{-INFINITY, -1};
+      if (more) {
+        const float2 r = __ldg(mine + static_cast<long long>(j) * ldp);
+        if (r.x > kFloor) e = Entry{r.x, __float_as_int(r.y)};
+      }
+      more = take_entries<K>(top, e, lane);   // a tile's entries fall: no later one can go in either
+      if (!__any_sync(0xffffffffu, more)) break;
+    }
+    if (lane < out.n_top) {
+      const long long at = static_cast<long long>(i) * out.n_top + lane;
+      out.top_ids[at] = top.id;
+      out.top_logp[at] = top.id >= 0 ? static_cast<float>((top.v - m0) - l0) : -INFINITY;
+    }
   }
 }
 
@@ -396,12 +411,16 @@ int stats_tiles(bool bf16, int V) { return (V + (bf16 ? kBN : 32) - 1) / (bf16 ?
 
 namespace {
 
+// Up to this many positions a whole block joins each one's tiles.
+constexpr int kWideFinish = 1024;
+
 template <int K>
 cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const StatsBuf& b, int n,
                        int V, int d, const int* y, int sms, int* sync, const DevCtl& ctl,
                        cudaStream_t st) {
   if (K > 0) {
-    const cudaError_t e = cudaMemsetAsync(b.tau, 0, sizeof(uint32_t) * n, st);
+    const cudaError_t e = 
+        cudaMemsetAsync(b.tau, 0, sizeof(uint32_t) * static_cast<size_t>(K) * b.ldp, st);
     if (e != cudaSuccess) return e;
   }
   typename EpiStats<K>::Params p{y, b.part, b.tsum, b.zy, b.tau, b.list, n, V, b.ldp};
@@ -410,10 +429,16 @@ cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const S
 }
 
 template <int K>
-cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, const int* y,
+cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, bool stream,
+                         const int* y,
                          const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
-  k_stats_finish<K><<<(n + 7) / 8, 256, 0, st>>>(b.part, b.tsum, b.list, with_tau ? b.tau : nullptr,
-                                                 b.zy, y, n, S, V, b.ldp, out, ctl);
+  const uint32_t* tau = with_tau ? b.tau : nullptr;
+  if (n <= kWideFinish)
+    k_stats_finish<K, 8><<<n, 256, 0, st>>>(b.part, b.tsum, b.list, tau, b.zy, y, n, S, V, b.ldp,
+                                            stream, out, ctl);
+  else
+    k_stats_finish<K, 1><<<(n + 7) / 8, 256, 0, st>>>(b.part, b.tsum, b.list, tau, b.zy, y, n, S, V,
+                                                      b.ldp, stream, out, ctl);
   return cudaGetLastError();
 }
 
@@ -445,12 +470,12 @@ cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_stats_finish(const StatsBuf& b, bool bf16, int n_top, int n, int V, const int* y,
-                                float* logp, float* entropy, float* lse, int* top_ids,
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, bool stream, int n_top,
+                                int n, int V, const int* y, float* logp, float* entropy, float* lse, int* top_ids,
                                 float* top_logp, const DevCtl& ctl, cudaStream_t st) {
   const StatsOut out{logp, entropy, lse, top_logp, top_ids, n_top};
-  return DPO_BY_LIST(stats_list_len(n_top), stats_finish)(b, bf16, n, stats_tiles(bf16, V), V, y,
-                                                          out, ctl, st);
+  return DPO_BY_LIST(stats_list_len(n_top), stats_finish)(b, thresholds, n, S, V, stream, y, out, ctl,
+                                                          st);
 }
 
 }  // namespace dpo

@@ -1,0 +1,165 @@
+// Shared by the token statistics kernels: joining sums of tiles, and lists of the largest logits
+// spread over a warp.
+#pragma once
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+
+namespace dpo {
+
+constexpr float kLog2eS = 1.4426950408889634f;
+constexpr float kLn2S = 0.6931471805599453f;
+// Logits at or below this count as -inf: they add nothing and are no alternative.
+constexpr float kFloor = -1e30f;
+
+// Order-preserving map of floats to unsigned integers; 0 is below every float's image.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);           // -0 counts as 0
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  if (o == 0) return -INFINITY;
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+
+// ------------------------------------------------------------------ lists across a warp
+// A falling list of 32 (logit, id) entries, entry j in lane j.
+struct Entry {
+  float v;
+  int id;
+};
+
+__device__ __forceinline__ bool ahead(const Entry& a, const Entry& b) {
+  return a.v > b.v || (a.v == b.v && a.id < b.id);
+}
+
+// The 32 best of two falling lists: entry j against entry 31 - j of the other leaves the best
+// 32 in an order that falls and then rises (or the reverse), which five exchange rounds sort.
+__device__ __forceinline__ void merge_lists(Entry& a, Entry b, int lane) {
+  b.v = __shfl_sync(0xffffffffu, b.v, 31 - lane);
+  b.id = __shfl_sync(0xffffffffu, b.id, 31 - lane);
+  if (ahead(b, a)) a = b;
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const Entry o{__shfl_xor_sync(0xffffffffu, a.v, w), __shfl_xor_sync(0xffffffffu, a.id, w)};
+    if (((lane & w) == 0) == ahead(o, a)) a = o;
+  }
+}
+
+// Puts x into a falling list (entry j in lane j), behind every entry ahead of it.
+__device__ __forceinline__ void insert_entry(Entry& list, const Entry& x, int lane) {
+  const int at = __popc(__ballot_sync(0xffffffffu, ahead(list, x)));
+  const Entry up{__shfl_up_sync(0xffffffffu, list.v, 1), __shfl_up_sync(0xffffffffu, list.id, 1)};
+  if (lane == at) list = x;
+  else if (lane > at) list = up;
+}
+
+// Puts every lane's e (id >= 0) into a falling list of which the first K count, as far as it is
+// ahead of the K-th. Returns whether this lane's was when the call began.
+template <int K>
+__device__ __forceinline__ bool take_entries(Entry& list, const Entry& e, int lane) {
+  auto fits = [&] {
+    const Entry last{__shfl_sync(0xffffffffu, list.v, K - 1),
+                     __shfl_sync(0xffffffffu, list.id, K - 1)};
+    return e.id >= 0 && (last.id < 0 || ahead(e, last));
+  };
+  const bool first = fits();
+  uint32_t hit = __ballot_sync(0xffffffffu, first);
+  while (hit) {
+    const int src = __ffs(hit) - 1;
+    insert_entry(list, Entry{__shfl_sync(0xffffffffu, e.v, src),
+                             __shfl_sync(0xffffffffu, e.id, src)}, lane);
+    hit &= hit - 1;
+    hit &= __ballot_sync(0xffffffffu, fits());
+  }
+  return first;
+}
+
+// Running maximum, S and T of a set of tiles (S and T in fp64, so that a vocabulary of millions
+// loses nothing).
+struct Sums {
+  float M = -INFINITY;
+  double s = 0.0, t = 0.0;
+  __device__ __forceinline__ void join(float m, double s2, double t2) {
+    if (m == -INFINITY) return;
+    if (m > M) {
+      if (M != -INFINITY) {
+        const double f = expf(M - m), back = M - m;
+        t = f * (t + s * back) + t2;
+        s = f * s + s2;
+      } else {
+        s = s2;
+        t = t2;
+      }
+      M = m;
+    } else {
+      const double f = expf(m - M), back = m - M;
+      t += f * (t2 + s2 * back);
+      s += f * s2;
+    }
+  }
+};
+
+// Sorted insert into a thread's own falling list; among equal logits the earlier one stays in
+// front.
+template <int K>
+__device__ __forceinline__ void insert_sorted(float (&val)[K], int (&id)[K], float x, int xi) {
+#pragma unroll
+  for (int j = K - 1; j > 0; --j) {
+    const bool here = x > val[j], above = x > val[j - 1];
+    id[j] = above ? id[j - 1] : (here ? xi : id[j]);
+    val[j] = above ? val[j - 1] : (here ? x : val[j]);
+  }
+  if (x > val[0]) {
+    val[0] = x;
+    id[0] = xi;
+  }
+}
+
+// ------------------------------------------------------------------ the streaming form's split
+constexpr int kSRows = kStreamRows;
+constexpr int kSPiece = 8;       // rows the short tiles are cut at
+constexpr int kSSegs = kStreamLists;   // threads per position, and a thread's rows of a tile
+constexpr int kSegRows = kSRows / kSSegs;
+constexpr int kSWarps = 8;       // warps that take positions
+
+// Which vocabulary rows a CTA takes: whole tiles side by side, then its share of the rest in
+// pieces of kSPiece rows.
+struct StreamSplit {
+  int V, ctas, waves, rest0, pieces;      // rest0: first row after the whole waves
+  __device__ __forceinline__ StreamSplit(int V_, int ctas_) : V(V_), ctas(ctas_) {
+    waves = V / (kSRows * ctas);
+    rest0 = waves * kSRows * ctas;
+    pieces = (V - rest0 + kSPiece - 1) / kSPiece;
+  }
+  __device__ __forceinline__ int rest(int cta) const {       // first row of the CTA's share
+    return rest0 + static_cast<int>(static_cast<long long>(pieces) * cta / ctas) * kSPiece;
+  }
+  __device__ __forceinline__ int tiles(int cta) const {
+    return waves + (rest(cta + 1) > rest(cta) ? 1 : 0);
+  }
+  __device__ __forceinline__ void tile(int cta, int t, int& r0, int& rows) const {
+    if (t < waves) {
+      r0 = (t * ctas + cta) * kSRows;
+      rows = kSRows;
+    } else {
+      r0 = rest(cta);
+      rows = min(V, rest(cta + 1)) - r0;
+    }
+  }
+  // The CTA and the row within its tile that vocabulary row v went to.
+  __device__ __forceinline__ void owner(int v, int& cta, int& row) const {
+    if (v < rest0) {
+      cta = v / kSRows % ctas;
+      row = v % kSRows;
+    } else {
+      const long long q = (v - rest0) / kSPiece;             // the last cta with rest(cta) <= v
+      cta = static_cast<int>(((q + 1) * ctas - 1) / pieces);
+      row = v - rest(cta);
+    }
+  }
+};
+
+}  // namespace dpo

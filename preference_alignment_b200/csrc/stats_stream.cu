@@ -1,0 +1,430 @@
+// Token statistics of a few positions (a serving step): the head's weight is read once and that
+// is the time, so the kernel is a stream of W through the tensor cores.
+//
+// Orientation: W rows are the accumulator's 128 lanes and the NT positions its columns, z^T = W .
+// Hp^T, so a pipeline stage is 16 KiB of W and only NT * 128 bytes of hidden rows (the other
+// orientation pads a few positions to 128 rows, 16 KiB a stage). The CTAs walk W side by side,
+// tile t of 128 rows going to CTA t mod gridDim, and what does not fill a last wave is cut into
+// equal pieces: a short last tile each, whose missing rows are not loaded. (One contiguous range
+// per CTA reads 148 places of W at a time instead of one: 187 us instead of 164 us at V = 128,256,
+// d = 4096.) Every running value stays on chip until the CTA is done, so a position leaves one set
+// of sums per CTA, not one per tile.
+//
+// Roles (320 threads): warp 0 issues the TMA loads, warp 1 owns TMEM and issues the MMAs, warps
+// 2-9 turn the accumulator around through shared memory (z[position][vocabulary row]); then each
+// thread has one position and one segment of a tile's rows, keeps the running maximum, S, T and
+// its K largest logits in registers.
+#include "internal.h"
+#include "stats.cuh"
+
+namespace dpo {
+
+namespace {
+
+constexpr int kSWBytes = kSRows * kBK * 2;     // 16 KiB of W per stage
+constexpr int kSThreads = (2 + kSWarps) * 32;
+
+template <int NT>
+struct StreamShape {
+  static constexpr int kStages = NT == 64 ? 7 : NT == 32 ? 10 : 11;
+  static constexpr int kHBytes = NT * kBK * 2;
+  static constexpr int kStage = kSWBytes + kHBytes;
+  static constexpr int kPitch = kSRows + 1;                // of z: odd, so columns spread over banks
+  static constexpr int kZ = NT * kPitch * 4;               // z[position][row], later the sums
+  static constexpr int kSmem =
+      kStages * kStage + kZ + NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
+  static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
+  static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
+};
+
+// 8, 16 or 32 consecutive fp32 columns of this warp's 32 TMEM lanes.
+template <int N>
+__device__ __forceinline__ void tmem_cols(uint32_t addr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) {
+    tmem_ld32(addr, r);
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+  } else {
+    static_assert(N == 8, "8, 16 or 32 columns");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr));
+  }
+}
+
+// Barrier over the kSWarps position warps.
+__device__ __forceinline__ void warps_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kSWarps * 32) : "memory");
+}
+// The same barrier, joined with an AND over its threads: every warp takes the same decision to
+// go on or to leave, so none is left waiting in it.
+__device__ __forceinline__ bool warps_all(bool mine) {
+  int all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(mine ? 1 : 0), "n"(kSWarps * 32)
+      : "memory");
+  return all != 0;
+}
+
+struct StreamArgs {
+  const int* y;         // given tokens, or nullptr
+  float2* part;         // [gridDim.x, ldp]
+  float* tsum;          // [gridDim.x, ldp]
+  float* zy;            // [ldp]
+  uint32_t* tau;        // [K groups, ldp] thresholds, zeroed before the launch
+  float2* list;         // [gridDim.x * kSSegs, K, ldp]
+  int n, V, k_blocks, ldp;
+  int share;            // rows of tmWp's boxes: the largest share of what the whole waves leave
+};
+
+template <int NT, int K>
+__global__ void __launch_bounds__(kSThreads, 1)
+    k_stats_stream(const __grid_constant__ CUtensorMap tmW,
+                   const __grid_constant__ CUtensorMap tmWp,
+                   const __grid_constant__ CUtensorMap tmH, StreamArgs a, DevCtl ctl) {
+  using Sh = StreamShape<NT>;
+  constexpr int kStages = Sh::kStages;
+  constexpr int kList = K > 0 ? K : 1;
+  constexpr int kPitch = Sh::kPitch;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sW = smem;
+  uint8_t* sH = sW + kStages * kSWBytes;
+  float* z = reinterpret_cast<float*>(sH + kStages * Sh::kHBytes);
+  int* sy = reinterpret_cast<int*>(z + NT * Sh::kPitch);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sy + NT);
+  // bars: [0, S) full, [S, 2S) empty, 2S + {0,1} acc_full, 2S + {2,3} acc_empty, 2S + 4 drain
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t full0 = smem_u32(bars);
+  const uint32_t empty0 = smem_u32(bars + kStages);
+  const uint32_t accf0 = smem_u32(bars + 2 * kStages);
+  const uint32_t acce0 = smem_u32(bars + 2 * kStages + 2);
+  const uint32_t drain = smem_u32(bars + 2 * kStages + 4);
+
+  const StreamSplit split(a.V, gridDim.x);
+  const int tiles = split.tiles(blockIdx.x);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(accf0 + 8 * b, 1);
+      mbar_init(acce0 + 8 * b, kSWarps * 32);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmWp);
+    tma_prefetch_desc(&tmH);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Sh::kTmem);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < NT; i += kSThreads)
+    sy[i] = a.y != nullptr && i < a.n ? __ldg(a.y + i) : -1;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  uint32_t issued_mask = 0, issued_par = 0;   // for the teardown, as in the GEMM kernels
+
+  if (warp == 0 && lane == 0) {
+    // ---------------------------------------------------------------- TMA producer
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = 0; t < tiles && ok; ++t) {
+      int r0, rows;
+      split.tile(blockIdx.x, t, r0, rows);
+      const bool whole = t < split.waves;
+      const uint32_t bytes = (whole ? kSRows : a.share) * kBK * 2 + Sh::kHBytes;
+      for (int kb = 0; kb < a.k_blocks; ++kb) {
+        if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, ctl, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = full0 + 8 * stage;
+        mbar_arrive_expect_tx(fb, bytes);
+        const uint32_t w_dst = smem_u32(sW + stage * kSWBytes);
+        tma_load_2d(w_dst, whole ? &tmW : &tmWp, fb, kb * kBK, r0);
+        tma_load_2d(smem_u32(sH + stage * Sh::kHBytes), &tmH, fb, kb * kBK, 0);
+        issued_mask |= 1u << stage;
+        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok) {
+      record_status(ctl, kStatusTimeout);
+      *abort_flag = 1;
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ---------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc = idesc_bf16_f32(kSRows, NT, false, false);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = 0; t < tiles && ok; ++t) {
+      const int acc = t & 1;
+      if (!mbar_wait(acce0 + 8 * acc, ((t >> 1) & 1) ^ 1, ctl, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int kb = 0; kb < a.k_blocks; ++kb) {
+        if (!mbar_wait(full0 + 8 * stage, phase, ctl, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t w0 = smem_u32(sW + stage * kSWBytes);
+        const uint32_t h0 = smem_u32(sH + stage * Sh::kHBytes);
+#pragma unroll
+        for (int k = 0; k < kBK / 16; ++k)
+          tc_mma_f16(tmem_base + acc * NT, sw128_desc(w0 + k * 32, 16, 1024),
+                     sw128_desc(h0 + k * 32, 16, 1024), idesc, (kb != 0 || k != 0) ? 1u : 0u);
+        tc_commit(empty0 + 8 * stage);
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      tc_commit(accf0 + 8 * acc);
+    }
+    if (!ok) {
+      record_status(ctl, kStatusTimeout);
+      *abort_flag = 1;
+    }
+    tc_commit(drain);                       // no MMA may be in flight when TMEM is freed
+    volatile int never = 0;
+    if (!mbar_wait(drain, 0, ctl, &never)) record_status(ctl, kStatusTimeout);
+  } else if (warp >= 2) {
+    // ---------------------------------------------------------------- positions
+    const int pt = threadIdx.x - 64;
+    const int quad = warp & 3;              // TMEM lanes this warp may read
+    constexpr int kCols = NT / 2;           // and its half of the columns
+    const int c0 = ((warp - 2) >> 2) * kCols;
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const int p = pt % NT, seg = pt / NT;   // this thread's position and segment
+    const bool mine = pt < NT * kSSegs && p < a.n;
+    const int set = blockIdx.x * kSSegs + seg;
+    float m = kFloor, s = 0.f, tt = 0.f;
+    float val[kList];
+    int id[kList];
+#pragma unroll
+    for (int j = 0; j < kList; ++j) {
+      val[j] = kFloor;
+      id[j] = -1;
+    }
+    bool ok = true;
+    for (int t = 0; t < tiles; ++t) {
+      // the groups' thresholds: asked for before the wait for the tile
+      uint32_t th = 0xffffffffu, bid = 0;
+      if (K > 0 && mine) {
+#pragma unroll
+        for (int g = 0; g < kList; ++g) {
+          const uint32_t o = __ldcg(a.tau + static_cast<long long>(g) * a.ldp + p);
+          th = min(th, o);
+          if (g == set % kList) bid = o;
+        }
+      }
+      const int acc = t & 1;
+      ok = mbar_wait(accf0 + 8 * acc, (t >> 1) & 1, ctl, abort_flag);
+      // also: every warp is done with the last tile's z
+      if (!warps_all(ok)) {
+        if (!ok) record_status(ctl, kStatusTimeout);
+        *abort_flag = 1;
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      {
+        uint32_t v[kCols];
+        tmem_cols<kCols>(tmem_base + lanes + acc * NT + c0, v);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(acce0 + 8 * acc);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c)
+          z[(c0 + c) * kPitch + quad * 32 + lane] = __uint_as_float(v[c]);
+      }
+      warps_sync();
+      int r0, rows;
+      split.tile(blockIdx.x, t, r0, rows);
+      const float* zp = z + p * kPitch + (seg % kSSegs) * kSegRows;
+      float x[kSegRows];
+      float cm = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < kSegRows; ++j) {
+        x[j] = seg * kSegRows + j < rows ? zp[j] : -INFINITY;
+        cm = fmaxf(cm, x[j]);
+      }
+      if (mine && seg == 0 && sy[p] >= r0 && sy[p] < r0 + rows) a.zy[p] = z[p * kPitch + sy[p] - r0];
+      // rounded products (no fused multiply-add): back is exactly 0 while the maximum stands
+      const float nm = fmaxf(m, cm);
+      const float nref = __fmul_rn(nm, kLog2eS);
+      const float back = __fmul_rn(m, kLog2eS) - nref;
+      const float f = ex2_approx(back);
+      tt = f * fmaf(s, back, tt);
+      s *= f;
+      m = nm;
+#pragma unroll
+      for (int j = 0; j < kSegRows; ++j) {
+        const float b = fmaf(x[j], kLog2eS, -nref);
+        const float ex = ex2_approx(b);
+        s += ex;
+        tt = fmaf(ex, fmaxf(b, -1e30f), tt);               // the bound keeps 0 * -inf out of T
+      }
+      if (K > 0) {
+        const float tauv = from_ordered(th);
+        uint32_t hit = 0;
+        if (mine && cm >= tauv && cm > val[kList - 1]) {
+#pragma unroll
+          for (int j = 0; j < kSegRows; ++j)
+            hit |= (x[j] >= tauv && x[j] > val[kList - 1] ? 1u : 0u) << j;
+        }
+        if (__any_sync(0xffffffffu, hit != 0)) {
+          while (hit != 0) {
+            const int j = __ffs(hit) - 1;
+            hit &= hit - 1;
+            insert_sorted<kList>(val, id, zp[j], r0 + seg * kSegRows + j);
+          }
+          // the set's largest logit is its group's bid for the threshold
+          if (mine && ordered(val[0]) > bid && val[0] > kFloor)
+            atomicMax(a.tau + static_cast<long long>(set % kList) * a.ldp + p, ordered(val[0]));
+        }
+      }
+    }
+    // a position's segments join in a fixed order, in z's place; one set of sums per CTA
+    if (warps_all(ok)) {
+      const float r = fmaf(-m, kLog2eS, __fmul_rn(m, kLog2eS));   // what m * log2(e) lost
+      if (seg < kSSegs) {
+        float* q = z + (seg * NT + p) * 3;
+        q[0] = m;
+        q[1] = fmaf(s, r * kLn2S, s);
+        q[2] = fmaf(s, r, tt) * kLn2S;
+      }
+      warps_sync();
+      if (mine && seg == 0) {
+        Sums j;
+        for (int g = 0; g < kSSegs; ++g) {
+          const float* w = z + (g * NT + p) * 3;
+          j.join(w[0], w[1], w[2]);
+        }
+        const long long to = static_cast<long long>(blockIdx.x) * a.ldp + p;
+        a.part[to] = make_float2(j.M, static_cast<float>(j.s));
+        a.tsum[to] = static_cast<float>(j.t);
+      }
+      if (K > 0 && mine) {
+        float2* l = a.list + static_cast<long long>(set) * kList * a.ldp + p;
+#pragma unroll
+        for (int j = 0; j < kList; ++j)
+          l[static_cast<long long>(j) * a.ldp] = make_float2(val[j], __int_as_float(id[j]));
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  __syncthreads();
+  if (warp == 0 && lane == 0 && *abort_flag) {
+    // after an abort, loads may still be landing: wait (bounded) for each stage's last one
+    volatile int never = 0;
+    DevCtl c2 = ctl;
+    c2.budget_ns = ctl.budget_ns / 4 + 1000000ull;
+    for (int s = 0; s < kStages; ++s)
+      if (issued_mask & (1u << s))
+        (void)mbar_wait(full0 + 8 * s, (issued_par >> s) & 1u, c2, &never);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Sh::kTmem);
+  }
+}
+
+template <int NT, int K>
+cudaError_t stream_launch(const CUtensorMap& mW, const CUtensorMap& mWp, const CUtensorMap& mH,
+                          const StreamArgs& a, int grid, const DevCtl& ctl, cudaStream_t st) {
+  auto kern = k_stats_stream<NT, K>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             StreamShape<NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kSThreads, StreamShape<NT>::kSmem, st>>>(mW, mWp, mH, a, ctl);
+  return cudaGetLastError();
+}
+
+template <int K>
+cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mWp,
+                                const CUtensorMap& mH, const StreamArgs& a, int grid,
+                                const DevCtl& ctl, cudaStream_t st) {
+  switch (stats_stream_cols(a.n)) {
+    case 16: return stream_launch<16, K>(mW, mWp, mH, a, grid, ctl, st);
+    case 32: return stream_launch<32, K>(mW, mWp, mH, a, grid, ctl, st);
+    default: return stream_launch<64, K>(mW, mWp, mH, a, grid, ctl, st);
+  }
+}
+
+}  // namespace
+
+int stats_stream_cols(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : 64; }
+
+int stats_stream_ctas(int V, int sms) {
+  const int pieces = (V + kSPiece - 1) / kSPiece;
+  return pieces < sms ? pieces : sms;
+}
+
+int stats_stream_share(int V, int sms) {
+  const int ctas = stats_stream_ctas(V, sms < kStreamCtas ? sms : kStreamCtas);
+  const int rest = V - V / (kSRows * ctas) * kSRows * ctas;
+  const int pieces = (rest + kSPiece - 1) / kSPiece;
+  const int share = (pieces + ctas - 1) / ctas;
+  return (share > 0 ? share : 1) * kSPiece;
+}
+
+cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapWp,
+                                const CUtensorMap& mapH, const StatsBuf& b, int n_top, int n, int V,
+                                int d, const int* y, int sms, const DevCtl& ctl, cudaStream_t st) {
+  const int K = stats_list_len(n_top);
+  if (K > 0) {
+    const cudaError_t e =
+        cudaMemsetAsync(b.tau, 0, sizeof(uint32_t) * static_cast<size_t>(K) * b.ldp, st);
+    if (e != cudaSuccess) return e;
+  }
+  const StreamArgs a{y, b.part, b.tsum, b.zy, b.tau, b.list, n, V, (d + kBK - 1) / kBK, b.ldp,
+                     stats_stream_share(V, sms)};
+  const int grid = stats_stream_ctas(V, sms < kStreamCtas ? sms : kStreamCtas);
+  switch (K) {
+    case 0: return stream_by_positions<0>(mapW, mapWp, mapH, a, grid, ctl, st);
+    case 1: return stream_by_positions<1>(mapW, mapWp, mapH, a, grid, ctl, st);
+    case 8: return stream_by_positions<8>(mapW, mapWp, mapH, a, grid, ctl, st);
+    default: return stream_by_positions<32>(mapW, mapWp, mapH, a, grid, ctl, st);
+  }
+}
+
+}  // namespace dpo

@@ -114,6 +114,8 @@ CASES = [  # n, d, V, n_top
     (1, 8, 1, 1), (1, 64, 2, 5), (3, 72, 7, 8), (2, 64, 255, 9), (5, 64, 256, 1), (5, 136, 257, 32),
     (1, 512, 5000, 20), (33, 64, 1000, 0), (127, 64, 511, 8), (128, 64, 513, 7), (129, 200, 700, 32),
     (255, 64, 300, 2), (257, 128, 2050, 8), (300, 1024, 1300, 32), (700, 64, 260, 3),
+    (16, 72, 1184, 8), (17, 64, 9, 20), (32, 64, 19001, 8), (64, 64, 60001, 20), (64, 320, 2368, 32),
+    (65, 64, 3000, 8), (2, 64, 130000, 32), (50, 8, 40007, 1),
 ]
 
 
