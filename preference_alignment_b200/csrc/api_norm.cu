@@ -83,7 +83,7 @@ bool same_rows(const Span& a, const Span& b) {
 }
 
 dpo_status ckpt_ok(const dpo_checkpoint* c) {
-  if (c->codes == nullptr || c->scales == nullptr || !aligned16(c->codes))
+  if (c->codes == nullptr || c->scales == nullptr || !aligned16(c->codes) || !aligned4(c->scales))
     return DPO_ERR_INVALID_ARG;
   return DPO_OK;
 }
@@ -119,7 +119,9 @@ dpo_status norm_ok(const dpo_norm* n, NormIn* in, Span* x) {
   return DPO_OK;
 }
 
-size_t norm_ws_bytes(int32_t d) { return sizeof(float) * 2 * kNormParts * static_cast<size_t>(d); }
+size_t norm_ws_bytes(int32_t d) {
+  return sizeof(float) * 2 * static_cast<size_t>(norm_parts(d)) * static_cast<size_t>(d);
+}
 
 }  // namespace
 
@@ -187,9 +189,11 @@ dpo_status dpo_norm_forward(const dpo_norm* norm, void* y, int64_t y_stride, flo
         !apart(codes_span(save, rows, d), scales_span(save, rows, d)))
       return DPO_ERR_INVALID_ARG;
   }
+  const int sms = device_sms();
+  if (sms < 1) return DPO_ERR_CUDA;
   return cuda_status(launch_norm_fwd(in, y, y_stride, mean, rstd,
                                      save != nullptr ? save->codes : nullptr,
-                                     save != nullptr ? save->scales : nullptr,
+                                     save != nullptr ? save->scales : nullptr, sms,
                                      static_cast<cudaStream_t>(stream)));
 }
 

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(kCkWarps * 32) k_ckpt_pack(Src x, int rows, in
 #pragma unroll
     for (int u = 0; u < kCkSteps; ++u) {
       const int col = c0 + (u * 32 + lane) * 8;
-      float f[8] = {};
+      float2 f[4] = {};
       if (col < d) Src::widen(raw[u], f);
       hold8(f, codes, scales, row, col, d, blocks, col < d);
     }
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kCkWarps * 32) k_ckpt_unpack(RowsQ8 x, int row
     for (int u = 0; u < kCkSteps; ++u) {
       const int col = c0 + (u * 32 + lane) * 8;
       if (col < d) {
-        float f[8];
+        float2 f[4];
         RowsQ8::widen(raw[u], f);
         y.store(row, col, f);
       }
@@ -78,7 +78,7 @@ cudaError_t launch_ckpt_unpack(bool bf16, int rows, int d, const int8_t* codes,
                                cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const int grid = (rows + kCkWarps - 1) / kCkWarps;
-  const RowsQ8 x{codes, scales, d, q_blocks(d)};
+  const RowsQ8 x{codes, scales, d, q_blocks(d), static_cast<long long>(rows) * q_blocks(d)};
   if (bf16)
     k_ckpt_unpack<<<grid, kCkWarps * 32, 0, st>>>(x, rows, d,
                                                   OutBf16{static_cast<uint16_t*>(y), stride});

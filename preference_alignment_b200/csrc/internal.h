@@ -202,11 +202,12 @@ struct NormGradBuf {
   long long dx_stride;
   float *dweight, *dbias;
   int accumulate;
-  float* ws;                       // [2, kNormParts, d]
+  float* ws;                       // [2, norm_parts(d), d]
 };
-constexpr int kNormParts = 296;    // partial weight gradients at most: two blocks per SM
+constexpr int kPlanSms = 148;      // SMs the workspace is planned for (a B200's)
+int norm_parts(int d);             // partial weight gradients the workspace has room for
 cudaError_t launch_norm_fwd(const NormIn& n, void* y, long long y_stride, float* mean, float* rstd,
-                            int8_t* codes, uint8_t* scales, cudaStream_t st);
+                            int8_t* codes, uint8_t* scales, int sms, cudaStream_t st);
 cudaError_t launch_norm_bwd(const NormIn& n, const NormGradBuf& g, int sms, cudaStream_t st);
 
 // 64-bit order-independent fingerprint of a device buffer into out (device).

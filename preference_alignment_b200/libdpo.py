@@ -110,11 +110,21 @@ def _ptr(x, kind: Optional[str] = None) -> Optional[int]:
     return ptr
 
 
+_raw_stream = None      # torch's lookup of a device's current stream as an address, once found
+
+
 def _stream(s) -> Optional[int]:
+    global _raw_stream
     if s is None:
+        if _raw_stream is not None:
+            return _raw_stream()
         try:
             import torch
             if torch.cuda.is_available():
+                found = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                current = torch.cuda.current_device
+                if found is not None:
+                    _raw_stream = lambda: found(current())  # noqa: E731
                 return torch.cuda.current_stream().cuda_stream
         except Exception:
             pass
@@ -467,42 +477,51 @@ MAX_TOP = 32                # DPO_MAX_TOP
 CHECKPOINT_BLOCK = 32       # DPO_CHECKPOINT_BLOCK
 NORM_KINDS = {"layer": 0, "rms": 1}
 
-_dtype_names = {}           # torch dtype -> its name, as _KINDS spells it
+_kinds = {}                 # torch dtype -> "bf16", "f32", "i32", "int8", "uint8" or its name
+_current_device = None
+
+
+def _name_of(x):
+    name = _kinds.get(x.dtype)
+    if name is None:
+        name = str(x.dtype).replace("torch.", "")
+        name = {"bfloat16": "bf16", "int16": "bf16", "uint16": "bf16", "float32": "f32",
+                "int32": "i32"}.get(name, name)
+        _kinds[x.dtype] = name
+    return name
 
 
 def _kind_of(x):
     """"bf16" or "f32" for a tensor of that element type, else a TypeError."""
     name = _name_of(x)
-    for kind in ("bf16", "f32"):
-        if name in _KINDS[kind]:
-            return kind
-    raise TypeError(f"expected a bf16 or f32 tensor, got {name}")
-
-
-def _name_of(x):
-    name = _dtype_names.get(x.dtype)
-    if name is None:
-        name = _dtype_names[x.dtype] = str(x.dtype).replace("torch.", "")
+    if name != "bf16" and name != "f32":
+        raise TypeError(f"expected a bf16 or f32 tensor, got {name}")
     return name
 
 
-def _on_device(x):
-    """The library works on the current device; a tensor elsewhere is refused."""
+def _device():
+    """The current device: what every buffer of a call has to be on."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        _current_device = torch.cuda.current_device
+    return _current_device()
+
+
+def _elsewhere(x, what):
     if not x.is_cuda:
-        raise ValueError(f"buffer of shape {tuple(x.shape)} is not in device memory")
-    import torch
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"buffer on {x.device}, but the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{what}: buffer of shape {tuple(x.shape)} is not in device memory")
+    raise ValueError(f"{what}: buffer on {x.device}, but the current device is cuda:{_device()}")
 
 
-def _buf(x, kind, n, what):
-    """Address of a dense device tensor of at least n elements of `kind`; None -> NULL, an
+def _buf(x, kind, n, what, dev):
+    """Address of a dense tensor of at least n elements of `kind` on device dev; None -> NULL, an
     integer address as it is."""
-    if x is None or isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    _on_device(x)
-    if _name_of(x) not in _KINDS.get(kind, (kind,)):
+    if not x.is_cuda or x.get_device() != dev:
+        _elsewhere(x, what)
+    if _kinds.get(x.dtype) != kind and _name_of(x) != kind:
         raise TypeError(f"{what}: expected a {kind} buffer, got {_name_of(x)}")
     if not x.is_contiguous():
         raise ValueError(f"{what}: buffer of shape {tuple(x.shape)} is not contiguous")
@@ -511,20 +530,37 @@ def _buf(x, kind, n, what):
     return x.data_ptr()
 
 
-def _row_view(x, what):
+def _row_view(x, what, dev):
     """(address, rows, d, stride) of a tensor of rows: 2-D with dense rows (any row stride), or
     contiguous of any shape with its last dimension the row."""
-    _on_device(x)
+    if not x.is_cuda or x.get_device() != dev:
+        _elsewhere(x, what)
     shape = x.shape
-    if len(shape) == 2 and x.stride(1) == 1 and shape[1] > 0:
+    if len(shape) == 2:
         rows, d = shape
-        return x.data_ptr(), rows, d, (x.stride(0) if rows > 1 else d)
+        stride, inner = x.stride()
+        if inner == 1 and d > 0:
+            return x.data_ptr(), rows, d, (stride if rows > 1 else d)
     if len(shape) == 0 or shape[-1] < 1 or not x.is_contiguous():
         raise ValueError(f"{what}: tensor of shape {tuple(shape)} has no dense rows")
     d = shape[-1]
     return x.data_ptr(), x.numel() // d, d, d
 
 
+def _work(ws, ws_bytes, dev):
+    """(address, bytes) of a workspace."""
+    if ws is not None and type(ws) is not int and (not ws.is_cuda or ws.get_device() != dev):
+        _elsewhere(ws, "ws")
+    if ws_bytes is None and type(ws) is not int and ws is not None:
+        ws_bytes = ws.numel() * ws.element_size()
+    return _ptr_of(ws), _nbytes(ws, ws_bytes)
+
+
+def _ptr_of(ws):
+    return ws if ws is None or type(ws) is int else ws.data_ptr()
+
+
+_vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _fns = {}
 
 
@@ -538,33 +574,60 @@ def _fn(name, argtypes):
     return fn
 
 
-_vp, _szp = ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)
-
-
 class TokenStatsOut(ctypes.Structure):
-    _fields_ = [("logp", _vp), ("entropy", _vp), ("lse_state", _vp), ("n_top", ctypes.c_int32),
+    _fields_ = [("logp", _vp), ("entropy", _vp), ("lse_state", _vp), ("n_top", _i32),
                 ("top_ids", _vp), ("top_logp", _vp)]
 
 
 class TokenRows(ctypes.Structure):
-    _fields_ = [("n", ctypes.c_int32), ("d", ctypes.c_int32), ("V", ctypes.c_int32),
-                ("dtype", ctypes.c_int32), ("H", _vp), ("h_stride", ctypes.c_int64), ("W", _vp),
-                ("tokens", _vp)]
+    _fields_ = [("n", _i32), ("d", _i32), ("V", _i32), ("dtype", _i32), ("H", _vp),
+                ("h_stride", _i64), ("W", _vp), ("tokens", _vp)]
 
 
-def _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp):
+class CheckpointC(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("scales", _vp)]
+
+
+class NormC(ctypes.Structure):
+    _fields_ = [("kind", _i32), ("dtype", _i32), ("weight_dtype", _i32), ("rows", _i32),
+                ("d", _i32), ("eps", ctypes.c_float), ("x", _vp), ("x_stride", _i64),
+                ("from_", ctypes.POINTER(CheckpointC)), ("weight", _vp), ("bias", _vp)]
+
+
+class NormGradsC(ctypes.Structure):
+    _fields_ = [("mean", _vp), ("rstd", _vp), ("dy", _vp), ("dy_dtype", _i32),
+                ("dy_stride", _i64), ("dx", _vp), ("dx_stride", _i64), ("dweight", _vp),
+                ("dbias", _vp), ("accumulate", _i32)]
+
+
+_szp, _batchp, _outp = ctypes.POINTER(_sz), ctypes.POINTER(Batch), ctypes.POINTER(TokenStatsOut)
+_rowsp, _ckptp = ctypes.POINTER(TokenRows), ctypes.POINTER(CheckpointC)
+_normp, _gradsp = ctypes.POINTER(NormC), ctypes.POINTER(NormGradsC)
+
+_STATS_SIZE = [_batchp, _i32, _szp, _szp]
+_STATS = [_batchp, _outp, _vp, _vp, _sz, _vp]
+_ROWS_SIZE = [_rowsp, _i32, _szp, _szp]
+_ROWS = [_rowsp, _outp, _vp, _sz, _vp]
+_PACK = [_i32, _i32, _i32, _vp, _i64, _ckptp, _vp]
+_UNPACK = [_i32, _i32, _i32, _ckptp, _vp, _i64, _vp]
+_NORM_FWD = [_normp, _vp, _i64, _vp, _vp, _ckptp, _vp]
+_NORM_WS = [_i32, _i32, _szp]
+_NORM_BWD = [_normp, _gradsp, _vp, _sz, _vp]
+
+
+def _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp, dev):
     n_top = int(n_top)
-    return TokenStatsOut(_buf(logp, "f32", n, "logp"), _buf(entropy, "f32", n, "entropy"),
-                         _buf(lse_state, "f32", n, "lse_state"), n_top,
-                         _buf(top_ids, "i32", n * n_top, "top_ids"),
-                         _buf(top_logp, "f32", n * n_top, "top_logp"))
+    return TokenStatsOut(_buf(logp, "f32", n, "logp", dev), _buf(entropy, "f32", n, "entropy", dev),
+                         _buf(lse_state, "f32", n, "lse_state", dev), n_top,
+                         _buf(top_ids, "i32", n * n_top, "top_ids", dev),
+                         _buf(top_logp, "f32", n * n_top, "top_logp", dev))
 
 
 def token_stats_size(batch: BatchArgs, n_top: int):
     """(bytes, min_bytes) of token_stats' workspace."""
-    a, b = ctypes.c_size_t(), ctypes.c_size_t()
-    fn = _fn("dpo_token_stats_size", [ctypes.POINTER(Batch), ctypes.c_int32, _szp, _szp])
-    _check(fn(ctypes.byref(batch.c), int(n_top), ctypes.byref(a), ctypes.byref(b)),
+    a, b = _sz(), _sz()
+    _check(_fn("dpo_token_stats_size", _STATS_SIZE)(ctypes.byref(batch.c), int(n_top),
+                                                    ctypes.byref(a), ctypes.byref(b)),
            "dpo_token_stats_size")
     return a.value, b.value
 
@@ -574,21 +637,21 @@ def token_stats(batch: BatchArgs, n_top: int, ws, logp=None, entropy=None, lse_s
     """dpo_token_stats: per scored position (row order) the target's log-prob, the entropy, the
     log-sum-exp that backward() reads and the n_top largest logits' ids and log-probs; per row
     the sum of the log-probs. Outputs left out are not written."""
-    out = _stats_out(batch.n_scored, n_top, logp, entropy, lse_state, top_ids, top_logp)
-    fn = _fn("dpo_token_stats", [ctypes.POINTER(Batch), ctypes.POINTER(TokenStatsOut), _vp, _vp,
-                                 ctypes.c_size_t, _vp])
-    _check(fn(ctypes.byref(batch.c), ctypes.byref(out), _buf(seq_logp, "f32", batch.c.R, "seq_logp"),
-              _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)), "dpo_token_stats")
+    dev = _device()
+    out = _stats_out(batch.n_scored, n_top, logp, entropy, lse_state, top_ids, top_logp, dev)
+    w, nbytes = _work(ws, ws_bytes, dev)
+    _check(_fn("dpo_token_stats", _STATS)(ctypes.byref(batch.c), ctypes.byref(out),
+                                          _buf(seq_logp, "f32", batch.c.R, "seq_logp", dev), w,
+                                          nbytes, _stream(stream)), "dpo_token_stats")
 
 
 def token_stats_rows_size(n: int, d: int, V: int, n_top: int, dtype="bf16"):
     """(bytes, min_bytes) of token_stats_rows' workspace."""
-    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    a, b = _sz(), _sz()
     rows = TokenRows(int(n), int(d), int(V), DTYPES[dtype] if isinstance(dtype, str) else int(dtype),
                      None, int(d), None, None)
-    fn = _fn("dpo_token_stats_rows_size",
-             [ctypes.POINTER(TokenRows), ctypes.c_int32, _szp, _szp])
-    _check(fn(ctypes.byref(rows), int(n_top), ctypes.byref(a), ctypes.byref(b)),
+    _check(_fn("dpo_token_stats_rows_size", _ROWS_SIZE)(ctypes.byref(rows), int(n_top),
+                                                        ctypes.byref(a), ctypes.byref(b)),
            "dpo_token_stats_rows_size")
     return a.value, b.value
 
@@ -597,21 +660,17 @@ def token_stats_rows(H, W, tokens, n_top: int, ws, logp=None, entropy=None, lse_
                      top_ids=None, top_logp=None, ws_bytes=None, stream=None):
     """dpo_token_stats_rows: token_stats for independent hidden rows, H [n, d] (any row stride)
     against W [V, d], tokens int32 [n] or None (then logp is None too)."""
-    h, n, d, stride = _row_view(H, "H")
+    dev = _device()
+    h, n, d, stride = _row_view(H, "H", dev)
     if len(W.shape) != 2 or W.shape[1] != d:
         raise ValueError(f"W of shape {tuple(W.shape)} does not fit rows of {d}")
     kind = _kind_of(H)
-    rows = TokenRows(n, d, W.shape[0], DTYPES[kind], h, stride, _buf(W, kind, 0, "W"),
-                     _buf(tokens, "i32", n, "tokens"))
-    out = _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp)
-    fn = _fn("dpo_token_stats_rows", [ctypes.POINTER(TokenRows), ctypes.POINTER(TokenStatsOut), _vp,
-                                      ctypes.c_size_t, _vp])
-    _check(fn(ctypes.byref(rows), ctypes.byref(out), _ptr(ws), _nbytes(ws, ws_bytes),
-              _stream(stream)), "dpo_token_stats_rows")
-
-
-class CheckpointC(ctypes.Structure):
-    _fields_ = [("codes", _vp), ("scales", _vp)]
+    rows = TokenRows(n, d, W.shape[0], DTYPES[kind], h, stride, _buf(W, kind, 0, "W", dev),
+                     _buf(tokens, "i32", n, "tokens", dev))
+    out = _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp, dev)
+    w, nbytes = _work(ws, ws_bytes, dev)
+    _check(_fn("dpo_token_stats_rows", _ROWS)(ctypes.byref(rows), ctypes.byref(out), w, nbytes,
+                                              _stream(stream)), "dpo_token_stats_rows")
 
 
 class Checkpoint:
@@ -633,59 +692,46 @@ class Checkpoint:
         return cls(torch.empty(rows, d, dtype=torch.int8, device=device),
                    torch.empty(rows, -(-d // CHECKPOINT_BLOCK), dtype=torch.uint8, device=device))
 
-    def _c(self):
-        return CheckpointC(_buf(self.codes, "int8", self.rows * self.d, "codes"),
-                           _buf(self.scales, "uint8", 0, "scales"))
+    def _c(self, dev):
+        return CheckpointC(_buf(self.codes, "int8", 0, "codes", dev),
+                           _buf(self.scales, "uint8", 0, "scales", dev))
 
 
 def _fits(rows, d, what, rows2, d2):
-    if (rows, d) != (rows2, d2):
+    if rows != rows2 or d != d2:
         raise ValueError(f"{what} is {rows2} x {d2}, expected {rows} x {d}")
 
 
 def checkpoint_pack(x, out: Checkpoint, stream=None):
     """dpo_checkpoint_pack: hold the rows of x (bf16 or f32, any row stride) in out."""
-    p, rows, d, stride = _row_view(x, "x")
+    dev = _device()
+    p, rows, d, stride = _row_view(x, "x", dev)
     _fits(rows, d, "out", out.rows, out.d)
-    c = out._c()
-    fn = _fn("dpo_checkpoint_pack", [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _vp,
-                                     ctypes.c_int64, ctypes.POINTER(CheckpointC), _vp])
-    _check(fn(DTYPES[_kind_of(x)], rows, d, p, stride, ctypes.byref(c), _stream(stream)),
+    c = out._c(dev)
+    _check(_fn("dpo_checkpoint_pack", _PACK)(DTYPES[_kind_of(x)], rows, d, p, stride,
+                                             ctypes.byref(c), _stream(stream)),
            "dpo_checkpoint_pack")
 
 
 def checkpoint_unpack(held: Checkpoint, y, stream=None):
     """dpo_checkpoint_unpack: the values held, into the rows of y (bf16 or f32)."""
-    p, rows, d, stride = _row_view(y, "y")
+    dev = _device()
+    p, rows, d, stride = _row_view(y, "y", dev)
     _fits(held.rows, held.d, "y", rows, d)
-    c = held._c()
-    fn = _fn("dpo_checkpoint_unpack", [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
-                                       ctypes.POINTER(CheckpointC), _vp, ctypes.c_int64, _vp])
-    _check(fn(DTYPES[_kind_of(y)], rows, d, ctypes.byref(c), p, stride, _stream(stream)),
+    c = held._c(dev)
+    _check(_fn("dpo_checkpoint_unpack", _UNPACK)(DTYPES[_kind_of(y)], rows, d, ctypes.byref(c), p,
+                                                 stride, _stream(stream)),
            "dpo_checkpoint_unpack")
 
 
-class NormC(ctypes.Structure):
-    _fields_ = [("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
-                ("weight_dtype", ctypes.c_int32), ("rows", ctypes.c_int32), ("d", ctypes.c_int32),
-                ("eps", ctypes.c_float), ("x", _vp), ("x_stride", ctypes.c_int64),
-                ("from_", ctypes.POINTER(CheckpointC)), ("weight", _vp), ("bias", _vp)]
-
-
-class NormGradsC(ctypes.Structure):
-    _fields_ = [("mean", _vp), ("rstd", _vp), ("dy", _vp), ("dy_dtype", ctypes.c_int32),
-                ("dy_stride", ctypes.c_int64), ("dx", _vp), ("dx_stride", ctypes.c_int64),
-                ("dweight", _vp), ("dbias", _vp), ("accumulate", ctypes.c_int32)]
-
-
-def _norm(x, kind_out, weight, bias, kind, eps):
+def _norm(x, kind_out, weight, bias, kind, eps, dev):
     """(NormC, rows, d) of a norm of x, a tensor of rows or a Checkpoint (then kind_out is the
     other side's element type)."""
     if isinstance(x, Checkpoint):
         p, rows, d, stride = None, x.rows, x.d, 0
-        held = ctypes.pointer(x._c())
+        held = ctypes.pointer(x._c(dev))
     else:
-        p, rows, d, stride = _row_view(x, "x")
+        p, rows, d, stride = _row_view(x, "x", dev)
         held = None
         kind_out = _kind_of(x)
     wkind = _kind_of(weight) if weight is not None else "f32"
@@ -695,8 +741,8 @@ def _norm(x, kind_out, weight, bias, kind, eps):
             raise TypeError(f"weight is {wkind}, bias {bkind}")
         wkind = bkind
     n = NormC(NORM_KINDS[kind] if isinstance(kind, str) else int(kind), DTYPES[kind_out],
-              DTYPES[wkind], rows, d, float(eps), p, stride, held,
-              _buf(weight, wkind, d, "weight"), _buf(bias, wkind, d, "bias"))
+              DTYPES[wkind], rows, d, eps, p, stride, held,
+              _buf(weight, wkind, d, "weight", dev), _buf(bias, wkind, d, "bias", dev))
     return n, rows, d
 
 
@@ -705,26 +751,28 @@ def norm_forward(x, y, weight=None, bias=None, kind="layer", eps=1e-5, mean=None
     """dpo_norm_forward: y = norm(x) by rows, kind "layer" or "rms"; mean and rstd (f32 [rows])
     are what norm_backward reads; save also holds x in 8 bits. x may be a Checkpoint: the norm
     of the values it holds."""
-    n, rows, d = _norm(x, _kind_of(y), weight, bias, kind, eps)
-    p, yr, yd, stride = _row_view(y, "y")
+    dev = _device()
+    ykind = _kind_of(y)
+    n, rows, d = _norm(x, ykind, weight, bias, kind, eps, dev)
+    p, yr, yd, stride = _row_view(y, "y", dev)
     _fits(rows, d, "y", yr, yd)
-    if DTYPES[_kind_of(y)] != n.dtype:
+    if DTYPES[ykind] != n.dtype:
         raise TypeError("y must have x's element type")
     c = None
     if save is not None:
         _fits(rows, d, "save", save.rows, save.d)
-        c = ctypes.byref(save._c())
-    fn = _fn("dpo_norm_forward", [ctypes.POINTER(NormC), _vp, ctypes.c_int64, _vp, _vp,
-                                  ctypes.POINTER(CheckpointC), _vp])
-    _check(fn(ctypes.byref(n), p, stride, _buf(mean, "f32", rows, "mean"),
-              _buf(rstd, "f32", rows, "rstd"), c, _stream(stream)), "dpo_norm_forward")
+        c = ctypes.byref(save._c(dev))
+    _check(_fn("dpo_norm_forward", _NORM_FWD)(ctypes.byref(n), p, stride,
+                                              _buf(mean, "f32", rows, "mean", dev),
+                                              _buf(rstd, "f32", rows, "rstd", dev), c,
+                                              _stream(stream)), "dpo_norm_forward")
 
 
 def norm_workspace_size(rows: int, d: int) -> int:
     """Workspace bytes of norm_backward."""
-    b = ctypes.c_size_t()
-    fn = _fn("dpo_norm_workspace_size", [ctypes.c_int32, ctypes.c_int32, _szp])
-    _check(fn(int(rows), int(d), ctypes.byref(b)), "dpo_norm_workspace_size")
+    b = _sz()
+    _check(_fn("dpo_norm_workspace_size", _NORM_WS)(int(rows), int(d), ctypes.byref(b)),
+           "dpo_norm_workspace_size")
     return b.value
 
 
@@ -733,19 +781,20 @@ def norm_backward(x, dy, mean, rstd, dx=None, weight=None, dweight=None, dbias=N
     """dpo_norm_backward: dx (x's element type; for a Checkpoint, its own), and the fp32 weight
     and bias gradients, from the forward's x (a tensor of rows or the Checkpoint that held it),
     its statistics and dy (bf16 or f32 rows)."""
-    n, rows, d = _norm(x, _kind_of(dx) if dx is not None else "bf16", weight, None, kind, 0.0)
-    p, yr, yd, stride = _row_view(dy, "dy")
+    dev = _device()
+    n, rows, d = _norm(x, _kind_of(dx) if dx is not None else "bf16", weight, None, kind, 0.0, dev)
+    p, yr, yd, stride = _row_view(dy, "dy", dev)
     _fits(rows, d, "dy", yr, yd)
     q, dx_stride = None, d
     if dx is not None:
-        q, xr, xd, dx_stride = _row_view(dx, "dx")
+        q, xr, xd, dx_stride = _row_view(dx, "dx", dev)
         _fits(rows, d, "dx", xr, xd)
         if DTYPES[_kind_of(dx)] != n.dtype:
             raise TypeError("dx must have x's element type")
-    g = NormGradsC(_buf(mean, "f32", rows, "mean"), _buf(rstd, "f32", rows, "rstd"), p,
-                   DTYPES[_kind_of(dy)], stride, q, dx_stride, _buf(dweight, "f32", d, "dweight"),
-                   _buf(dbias, "f32", d, "dbias"), 1 if accumulate else 0)
-    fn = _fn("dpo_norm_backward", [ctypes.POINTER(NormC), ctypes.POINTER(NormGradsC), _vp,
-                                   ctypes.c_size_t, _vp])
-    _check(fn(ctypes.byref(n), ctypes.byref(g), _ptr(ws), _nbytes(ws, ws_bytes), _stream(stream)),
-           "dpo_norm_backward")
+    g = NormGradsC(_buf(mean, "f32", rows, "mean", dev), _buf(rstd, "f32", rows, "rstd", dev), p,
+                   DTYPES[_kind_of(dy)], stride, q, dx_stride,
+                   _buf(dweight, "f32", d, "dweight", dev), _buf(dbias, "f32", d, "dbias", dev),
+                   1 if accumulate else 0)
+    w, nbytes = _work(ws, ws_bytes, dev)
+    _check(_fn("dpo_norm_backward", _NORM_BWD)(ctypes.byref(n), ctypes.byref(g), w, nbytes,
+                                               _stream(stream)), "dpo_norm_backward")
