@@ -423,8 +423,7 @@ dpo_status dpo_token_stats_rows(const dpo_token_rows* rows, const dpo_token_stat
 #define DPO_CHECKPOINT_BLOCK 32
 typedef struct {
   int8_t* codes;      /* device [rows, d], 16-byte aligned                               */
-  uint8_t* scales;    /* device [rows, ceil(d / 32)], 4-byte aligned: E + 127, or 255 for a
-                         NaN block                                                       */
+  uint8_t* scales;    /* device [rows, ceil(d / 32)]: E + 127, or 255 for a NaN block    */
 } dpo_checkpoint;
 
 /* Hold x (rows of d values of `dtype`, DPO_BF16 or DPO_F32, x_stride values apart) in `out`,

@@ -83,7 +83,7 @@ bool same_rows(const Span& a, const Span& b) {
 }
 
 dpo_status ckpt_ok(const dpo_checkpoint* c) {
-  if (c->codes == nullptr || c->scales == nullptr || !aligned16(c->codes) || !aligned4(c->scales))
+  if (c->codes == nullptr || c->scales == nullptr || !aligned16(c->codes))
     return DPO_ERR_INVALID_ARG;
   return DPO_OK;
 }

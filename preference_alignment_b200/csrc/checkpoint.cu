@@ -78,7 +78,7 @@ cudaError_t launch_ckpt_unpack(bool bf16, int rows, int d, const int8_t* codes,
                                cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   const int grid = (rows + kCkWarps - 1) / kCkWarps;
-  const RowsQ8 x{codes, scales, d, q_blocks(d), static_cast<long long>(rows) * q_blocks(d)};
+  const RowsQ8 x{codes, scales, d, q_blocks(d)};
   if (bf16)
     k_ckpt_unpack<<<grid, kCkWarps * 32, 0, st>>>(x, rows, d,
                                                   OutBf16{static_cast<uint16_t*>(y), stride});

@@ -221,6 +221,23 @@ cudaError_t launch_fingerprint(const void* data, unsigned long long bytes,
 enum GemmKind : int { kGemmForward = 0, kGemmGrad = 1, kGemmDH = 2, kGemmDW = 3 };
 int gemm_variant();
 
+// Launches a kernel that continues the one before it on the stream: it may take its place on the
+// GPU while that one still runs, and waits for its results with after_previous().
+template <class... KArgs, class... Args>
+cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, cudaStream_t st,
+                         Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
 // SMs of the current device (0 if the query failed).
 int device_sms();
 

@@ -9,11 +9,9 @@
 //
 // Forms by the row's length d, each row read once except in the last:
 //   d <= 256     a few lanes per row, one group of 8 values per lane
-//   forward      up to 16384: 1 or 4 warps per row, the row in registers
-//   backward     up to 8192: a block per row, one group per thread: a thread's columns stay the
-//                same from row to row, so the weight and its gradients stay in registers; rows
-//                arrive through a ring of cp.async slots, and R of them share a barrier
+//   d <= 16384   groups of 1 to 8 warps per row, the row in registers
 //   above        a block per row that reads it again (from L2) instead of holding it
+// The backward is in norm_bwd.cu.
 #include "norm.cuh"
 
 namespace dpo {
@@ -95,12 +93,14 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_rows(Src x, Out y, FwdArg
   const uint32_t slot = smem_u32(sb.p + 2 * vecs) + group * (NV * kLanes * Src::kSlot);
   const long long step = static_cast<long long>(gridDim.x) * groups;
   long long row = static_cast<long long>(blockIdx.x) * groups + group;
+  typename Src::Side side[NV];
   auto fetch = [&](long long r) {
     if (r < a.rows) {
 #pragma unroll
-      for (int u = 0; u < NV; ++u)
-        if ((u * kLanes + gl) * 8 < a.d)
-          x.fetch(slot, u * kLanes + gl, NV * kLanes, r, (u * kLanes + gl) * 8);
+      for (int u = 0; u < NV; ++u) {
+        x.fetch(slot, u * kLanes + gl, vecs, r);
+        if (u * kLanes + gl < vecs) side[u] = x.side(r, u * kLanes + gl);
+      }
     }
     cp_async_commit();
   };
@@ -117,15 +117,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_rows(Src x, Out y, FwdArg
   int turn = 0;
   for (; row < a.rows; row += step) {
     cp_async_wait<0>();
+    __syncwarp();
     float2 f[NV][4];
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-      const int col = (u * kLanes + gl) * 8;
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[u][j] = both(0.f);
-      if (col < a.d)
-        Src::widen(x.take(slot, u * kLanes + gl, NV * kLanes, row, col), f[u]);
+      if (u * kLanes + gl < vecs) Src::widen(Src::take(slot, u * kLanes + gl, side[u]), f[u]);
     }
+    __syncwarp();
     fetch(row + step);                                  // the slot is read: refill it
     float mu = 0.f;
     if (!a.rms) {
@@ -206,13 +206,13 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(Src x, Out y, Fw
   }
 }
 
-constexpr int kMaxFwd = 16384;          // longest row of the groups: 4 warps of 16 groups a lane
+constexpr int kMaxFwd = 16384;          // longest row of the groups: 8 warps of 8 groups a lane
 
-// As many warps as registers allow (about 8 NV + 50 a thread), in one block per SM so that the
+// As many warps as registers allow (about 8 NV + 60 a thread), in one block per SM so that the
 // weights are widened once; fewer where the rows do not fill them.
 template <class Src, class Out, int NV, int WG>
 cudaError_t fwd_rows(const Src& x, const Out& y, const FwdArgs& a, int sms, cudaStream_t st) {
-  constexpr int kThreads = NV > 8 ? 384 : NV > 4 ? 512 : 768;
+  constexpr int kThreads = NV > 4 ? 512 : 768;
   auto kern = k_norm_fwd_rows<Src, Out, NV, WG, kThreads>;
   const size_t vec = 2 * sizeof(float) * static_cast<size_t>(a.d);
   const size_t slot = static_cast<size_t>(NV) * WG * 32 * Src::kSlot;
@@ -233,9 +233,7 @@ cudaError_t fwd_by_length(const Src& x, const Out& y, const FwdArgs& a, int sms,
   if (nv <= 2) return fwd_rows<Src, Out, 2, WG>(x, y, a, sms, st);
   if (nv <= 4) return fwd_rows<Src, Out, 4, WG>(x, y, a, sms, st);
   if (nv <= 6) return fwd_rows<Src, Out, 6, WG>(x, y, a, sms, st);
-  if (nv <= 8) return fwd_rows<Src, Out, 8, WG>(x, y, a, sms, st);
-  if (nv <= 12) return fwd_rows<Src, Out, 12, WG>(x, y, a, sms, st);
-  return fwd_rows<Src, Out, 16, WG>(x, y, a, sms, st);
+  return fwd_rows<Src, Out, 8, WG>(x, y, a, sms, st);
 }
 
 template <class Src, class Out>
@@ -257,9 +255,12 @@ cudaError_t norm_fwd(const Src& x, const Out& y, const FwdArgs& a, int sms, cuda
     k_norm_fwd_wide<<<a.rows, kWideThreads, 0, st>>>(x, y, a);
     return cudaGetLastError();
   }
-  // one warp per row up to 16 groups a lane; 4 for longer rows, and where there are fewer rows
-  // than SMs, so that a row's latency is spread
+  // the fewest warps per row that leave a lane 8 groups (a row of 4,096 on one warp of 16 groups a
+  // lane: 51 us instead of 47 us for 16,384 rows, on four warps of 4: 47.5 us; at 2,048 one warp 27
+  // us, four 31 us); 4 where there are fewer rows than SMs, so that a row's latency is spread
+  if (a.d > 8192) return fwd_by_length<Src, Out, 8>(x, y, a, sms, st);
   if (a.d > 4096 || a.rows <= sms) return fwd_by_length<Src, Out, 4>(x, y, a, sms, st);
+  if (a.d > 2048) return fwd_by_length<Src, Out, 2>(x, y, a, sms, st);
   return fwd_by_length<Src, Out, 1>(x, y, a, sms, st);
 }
 

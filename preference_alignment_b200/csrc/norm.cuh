@@ -108,9 +108,6 @@ cudaError_t allow_smem(Kern kern, size_t bytes) {
                            : cudaSuccess;
 }
 
-inline RowsQ8 held_rows(const NormIn& n) {
-  const int nb = q_blocks(n.d);
-  return RowsQ8{n.codes, n.scales, n.d, nb, static_cast<long long>(n.rows) * nb};
-}
+inline RowsQ8 held_rows(const NormIn& n) { return RowsQ8{n.codes, n.scales, n.d, q_blocks(n.d)}; }
 
 }  // namespace dpo

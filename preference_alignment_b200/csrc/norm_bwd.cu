@@ -3,6 +3,7 @@
 //   d <= 256   a few lanes per row, one group of 8 values per lane
 //   d <= 8192  groups of 1 to 8 warps per row
 //   above      a block per row that reads it twice, and a column sum that reads it again
+#include "chain.cuh"
 #include "norm.cuh"
 
 namespace dpo {
@@ -60,6 +61,7 @@ __global__ void __launch_bounds__(kShortThreads) k_norm_bwd_short(X x, Dy dy, Dx
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = aw[j] = ab[j] = both(0.f);
   if (in) load_vec(a.weight, a.wbf16, col, 1.f, w);
+  let_next_start();
   // every thread of a warp makes the same number of rounds: the exchanges need them all
   const long long step = static_cast<long long>(gridDim.x) * kRows;
   const long long first = static_cast<long long>(blockIdx.x) * kRows;
@@ -139,20 +141,25 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
     if (r < a.rows) {
 #pragma unroll
       for (int u = 0; u < NV; ++u) {
-        const int k = u * kLanes + gl;
-        if (k < vecs) {
-          dy.fetch(slot, k, NV * kLanes, r, k * 8);
-          x.fetch(slot + kSlotDy, k, NV * kLanes, r, k * 8);
-        }
+        dy.fetch(slot, u * kLanes + gl, vecs, r);
+        x.fetch(slot + kSlotDy, u * kLanes + gl, vecs, r);
       }
     }
     cp_async_commit();
   };
+  let_next_start();
   fetch(row, ring);
   fetch(row + step, ring + kSlot);
-  // the statistics of the row after next are asked for a row ahead
+  // the next row's statistics and scales are asked for while this one is worked on
   auto stat = [&](const float* p, long long r) { return p != nullptr && r < a.rows ? __ldg(p + r) : 0.f; };
   float mu = kMean ? stat(a.mean, row) : 0.f, rs = stat(a.rstd, row);
+  typename X::Side side[NV];
+  auto sides = [&](long long r) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u)
+      if (r < a.rows && u * kLanes + gl < vecs) side[u] = x.side(r, u * kLanes + gl);
+  };
+  sides(row);
   for (int k = threadIdx.x; k < vecs; k += blockDim.x) {
     float2 f[4];
     load_vec(a.weight, a.wbf16, k * 8, 1.f, f);
@@ -169,6 +176,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
   for (; row < a.rows; row += step) {
     const uint32_t slot = ring + turn * kSlot;
     cp_async_wait<kSlots - 1>();
+    __syncwarp();
     const float mu2 = kMean ? stat(a.mean, row + step) : 0.f, rs2 = stat(a.rstd, row + step);
     float2 f[NV][4], e[NV][4];
     float c1 = 0.f, c2 = 0.f;
@@ -176,11 +184,13 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
     for (int u = 0; u < NV; ++u) {
       const int k = u * kLanes + gl;
       if (k < vecs) {
-        Dy::widen(dy.take(slot, k, NV * kLanes, row, k * 8), e[u]);
-        X::widen(x.take(slot + kSlotDy, k, NV * kLanes, row, k * 8), f[u]);
+        Dy::widen(Dy::take(slot, k, {}), e[u]);
+        X::widen(X::take(slot + kSlotDy, k, side[u]), f[u]);
       }
     }
+    __syncwarp();
     fetch(row + 2 * step, slot);                        // the slot is read: refill it
+    sides(row + step);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int k = u * kLanes + gl;
@@ -332,6 +342,7 @@ __global__ void __launch_bounds__(256) k_norm_dw_wide(X x, Dy dy, BwdArgs a) {
 __global__ void __launch_bounds__(256) k_norm_dw_sum(const float* pw, const float* pb, int n, int d,
                                                      float* dweight, float* dbias, int accumulate) {
   __shared__ float4 red[32][8];
+  after_previous();
   const float* p = blockIdx.y == 0 ? pw : pb;
   float* out = blockIdx.y == 0 ? dweight : dbias;
   if (out == nullptr) return;
@@ -341,7 +352,8 @@ __global__ void __launch_bounds__(256) k_norm_dw_sum(const float* pw, const floa
   if (col < d) {
 #pragma unroll 8
     for (int k = g; k < n; k += 32) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + static_cast<long long>(k) * d + col));
+      // past L1: this kernel may have started before the partials were written
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(p + static_cast<long long>(k) * d + col));
       s.x += v.x;
       s.y += v.y;
       s.z += v.z;
@@ -391,7 +403,7 @@ cudaError_t bwd_by_length(const X& x, const Dy& dy, const Dx& dx, const BwdArgs&
   if (a.d <= 512) return bwd_rows<X, Dy, Dx, 2, 1, kMean>(x, dy, dx, a, parts, sms, st);
   if (a.d <= 1024) return bwd_rows<X, Dy, Dx, 2, 2, kMean>(x, dy, dx, a, parts, sms, st);
   if (a.d <= 2048) return bwd_rows<X, Dy, Dx, 2, 4, kMean>(x, dy, dx, a, parts, sms, st);
-  if (a.d <= 4096) return bwd_rows<X, Dy, Dx, 4, 4, kMean>(x, dy, dx, a, parts, sms, st);
+  if (a.d <= 4096) return bwd_rows<X, Dy, Dx, 2, 8, kMean>(x, dy, dx, a, parts, sms, st);
   return bwd_rows<X, Dy, Dx, 4, 8, kMean>(x, dy, dx, a, parts, sms, st);
 }
 
@@ -433,9 +445,8 @@ cudaError_t norm_bwd(const X& x, const Dy& dy, const Dx& dx, BwdArgs a, float* w
     e = bwd_by_length<X, Dy, Dx, false>(x, dy, dx, a, &parts, sms, st);
   }
   if (e != cudaSuccess || (dweight == nullptr && dbias == nullptr)) return e;
-  k_norm_dw_sum<<<dim3((a.d + 31) / 32, 2), 256, 0, st>>>(a.pw, a.pb, parts, a.d, dweight, dbias,
-                                                          accumulate);
-  return cudaGetLastError();
+  return launch_after(k_norm_dw_sum, dim3((a.d + 31) / 32, 2), 256, st, a.pw, a.pb, parts, a.d,
+                      dweight, dbias, accumulate);
 }
 
 template <class X, class Dx>

@@ -4,8 +4,10 @@
 // and widened to fp32 (four pairs, for the packed fp32 instructions) when it is used.
 //
 // A source can also be fetched asynchronously (cp.async) into a slot of shared memory, kSlot
-// bytes per thread: each thread copies and later takes its own group, so no barrier stands
-// between the two, and the bytes in flight cost no registers.
+// bytes per group, so that the bytes in flight cost no registers. Group k of a row is taken by
+// lane k mod 32 of the warp that fetched groups k - k mod 32 .. + 31; lanes copy for one another,
+// so the warp synchronises between a copy's arrival and the takes, and between the takes and the
+// next fetch into the slot. Every lane of the warp calls, with the row's number of groups.
 #pragma once
 
 #include <cstdint>
@@ -24,11 +26,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-// 4 bytes, of which the first `bytes` are read and the rest zero.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes = 4) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -91,14 +88,16 @@ struct RowsBf16 {
   struct Raw {
     uint4 v;
   };
+  struct Side {};
   __device__ __forceinline__ Raw load(long long row, int col) const {
     return Raw{*reinterpret_cast<const uint4*>(p + row * stride + col)};
   }
-  __device__ __forceinline__ void fetch(uint32_t slot, int tid, int, long long row, int col) const {
-    cp_async16(slot + tid * 16, p + row * stride + col);
+  __device__ __forceinline__ void fetch(uint32_t slot, int k, int groups, long long row) const {
+    if (k < groups) cp_async16(slot + k * 16, p + row * stride + k * 8);
   }
-  __device__ __forceinline__ Raw take(uint32_t slot, int tid, int, long long, int) const {
-    return Raw{ld_shared_v4(slot + tid * 16)};
+  __device__ __forceinline__ Side side(long long, int) const { return Side{}; }
+  static __device__ __forceinline__ Raw take(uint32_t slot, int k, Side) {
+    return Raw{ld_shared_v4(slot + k * 16)};
   }
   static __device__ __forceinline__ void widen(const Raw& r, float2 (&f)[4]) { widen_bf16(r.v, f); }
 };
@@ -106,22 +105,35 @@ struct RowsBf16 {
 struct RowsF32 {
   const float* p;
   long long stride;
-  static constexpr int kSlot = 32;          // two planes of 16 bytes per thread
+  static constexpr int kSlot = 32;
   struct Raw {
     float4 a, b;
   };
+  struct Side {};
   __device__ __forceinline__ Raw load(long long row, int col) const {
     const float4* q = reinterpret_cast<const float4*>(p + row * stride + col);
     return Raw{q[0], q[1]};
   }
-  __device__ __forceinline__ void fetch(uint32_t slot, int tid, int threads, long long row,
-                                        int col) const {
-    const float* q = p + row * stride + col;
-    cp_async16(slot + tid * 16, q);
-    cp_async16(slot + (threads + tid) * 16, q + 4);
+  // A warp's 32 groups are 64 chunks of 16 bytes. A copy of two chunks per lane side by side
+  // would touch every 32-byte sector twice, half of it each time, and read twice the bytes from
+  // L2 (129 us instead of 83 us for a backward of 16384 x 4096): lane l copies chunks l and 32 + l.
+  // Chunk c lies at place c ^ (c / 8 mod 2), so that the takes of chunks 2 l and 2 l + 1 use all
+  // banks.
+  static __device__ __forceinline__ int place(int c) { return c ^ ((c >> 3) & 1); }
+  __device__ __forceinline__ void fetch(uint32_t slot, int k, int groups, long long row) const {
+    const int lane = k & 31, first = k - lane;
+    const float* q = p + row * stride + first * 8;
+    const int chunks = (groups - first) * 2;
+    if (lane < chunks) cp_async16(slot + first * 32 + place(lane) * 16, q + lane * 4);
+    if (lane + 32 < chunks)
+      cp_async16(slot + first * 32 + place(lane + 32) * 16, q + (lane + 32) * 4);
   }
-  __device__ __forceinline__ Raw take(uint32_t slot, int tid, int threads, long long, int) const {
-    const uint4 a = ld_shared_v4(slot + tid * 16), b = ld_shared_v4(slot + (threads + tid) * 16);
+  __device__ __forceinline__ Side side(long long, int) const { return Side{}; }
+  static __device__ __forceinline__ Raw take(uint32_t slot, int k, Side) {
+    const int lane = k & 31;
+    const uint32_t base = slot + (k - lane) * 32;
+    const uint4 a = ld_shared_v4(base + place(2 * lane) * 16);
+    const uint4 b = ld_shared_v4(base + place(2 * lane + 1) * 16);
     return Raw{make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z),
                            __uint_as_float(a.w)),
                make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z),
@@ -137,32 +149,26 @@ struct RowsF32 {
 
 struct RowsQ8 {
   const int8_t* codes;
-  const uint8_t* scales;                    // 4-byte aligned
+  const uint8_t* scales;
   int d, blocks;
-  long long n_scales;                       // bytes of scales
-  static constexpr int kSlot = 12;          // a plane of 8 bytes, one of 4 (the scale's word)
+  static constexpr int kSlot = 8;
   struct Raw {
     uint2 v;
     uint32_t s;
   };
-  __device__ __forceinline__ long long scale_at(long long row, int col) const {
-    return row * blocks + col / kQBlock;
-  }
+  using Side = uint32_t;                    // the scale byte, asked for ahead into a register
   __device__ __forceinline__ Raw load(long long row, int col) const {
-    return Raw{*reinterpret_cast<const uint2*>(codes + row * d + col), scales[scale_at(row, col)]};
+    return Raw{*reinterpret_cast<const uint2*>(codes + row * d + col),
+               scales[row * blocks + col / kQBlock]};
   }
-  __device__ __forceinline__ void fetch(uint32_t slot, int tid, int threads, long long row,
-                                        int col) const {
-    cp_async8(slot + tid * 8, codes + row * d + col);
-    const long long at = scale_at(row, col) & ~3ll;        // its word, cut at the array's end
-    const long long left = n_scales - at;
-    cp_async4(slot + threads * 8 + tid * 4, scales + at, left < 4 ? static_cast<uint32_t>(left) : 4u);
+  __device__ __forceinline__ void fetch(uint32_t slot, int k, int groups, long long row) const {
+    if (k < groups) cp_async8(slot + k * 8, codes + row * d + k * 8);
   }
-  __device__ __forceinline__ Raw take(uint32_t slot, int tid, int threads, long long row,
-                                      int col) const {
-    const uint32_t word = ld_shared_u32(slot + threads * 8 + tid * 4);
-    const uint32_t byte = static_cast<uint32_t>(scale_at(row, col)) & 3u;
-    return Raw{ld_shared_v2(slot + tid * 8), (word >> (8 * byte)) & 255u};
+  __device__ __forceinline__ Side side(long long row, int k) const {
+    return __ldg(scales + row * blocks + k * 8 / kQBlock);
+  }
+  static __device__ __forceinline__ Raw take(uint32_t slot, int k, Side s) {
+    return Raw{ld_shared_v2(slot + k * 8), s};
   }
   static __device__ __forceinline__ void widen(const Raw& r, float2 (&f)[4]) {
     widen_codes(r.v, q_scale(r.s), f);

@@ -12,6 +12,7 @@
 #include <cmath>
 
 #include "internal.h"
+#include "chain.cuh"
 #include "gemm_launch.cuh"
 #include "stats.cuh"
 
@@ -199,13 +200,29 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
   const int i = WPP > 1 ? blockIdx.x : blockIdx.x * 8 + warp;
   const int w = WPP > 1 ? warp : 0;
   if (i >= n) return;                     // whole warps; whole blocks when WPP > 1
+  after_previous();
+  // what the kernel before wrote is read past L1 (__ldcg): this one may have started before it
+  constexpr int U = 4;
+  Entry first[U];                         // the streaming form's sets, asked for before the sums
+  const int sets = stream ? S * kSSegs : 0;
+  auto load_sets = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = base + (u * WPP + w) * 32 + lane;
+      first[u] = Entry{-INFINITY, -1};
+      if (k < sets) {
+        const float2 r = __ldcg(list + static_cast<long long>(k) * K * ldp + i);
+        if (r.x > kFloor) first[u] = Entry{r.x, __float_as_int(r.y)};
+      }
+    }
+  };
+  if (K > 0 && stream) load_sets(0);
+  uint32_t th = 0;
+  if (K > 0 && tau != nullptr)
+    th = lane < K ? __ldcg(tau + static_cast<long long>(lane) * ldp + i) : 0xffffffffu;
   Sums a;
   Entry best{-INFINITY, -1};              // tiles by their maximum
-  float tauv = -INFINITY;
-  if (K > 0 && tau != nullptr)
-    tauv = from_ordered(__reduce_min_sync(
-        0xffffffffu, lane < K ? __ldg(tau + static_cast<long long>(lane) * ldp + i) : 0xffffffffu));
-  constexpr int U = 4;
+  float tauv = 0.f;
   for (int base = 0; base < S; base += 32 * WPP * U) {
     float2 q[U];
     float tq[U];
@@ -215,10 +232,11 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
       q[u] = make_float2(-INFINITY, 0.f);
       tq[u] = 0.f;
       if (k < S) {
-        q[u] = __ldg(part + static_cast<long long>(k) * ldp + i);
-        tq[u] = __ldg(tsum + static_cast<long long>(k) * ldp + i);
+        q[u] = __ldcg(part + static_cast<long long>(k) * ldp + i);
+        tq[u] = __ldcg(tsum + static_cast<long long>(k) * ldp + i);
       }
     }
+    if (K > 0 && base == 0) tauv = from_ordered(__reduce_min_sync(0xffffffffu, th));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       a.join(q[u].x, q[u].y, tq[u]);
@@ -237,29 +255,16 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
     }
   }
   if (K > 0 && stream) {
-    const int sets = S * kSSegs;
     for (int base = 0; base < sets; base += 32 * WPP * U) {
-      Entry e[U];
+      if (base > 0) load_sets(base);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = base + (u * WPP + w) * 32 + lane;
-        e[u] = Entry{-INFINITY, -1};
-        if (k < sets) {
-          const float2 r = __ldg(list + static_cast<long long>(k) * K * ldp + i);
-          if (r.x > kFloor && r.x >= tauv) e[u] = Entry{r.x, __float_as_int(r.y)};
-        }
+        if (first[u].v < tauv) first[u].id = -1;
+        take_entries<K>(best, first[u], lane);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) take_entries<K>(best, e[u], lane);
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_down_sync(0xffffffffu, a.M, o);
-    const double s2 = __shfl_down_sync(0xffffffffu, a.s, o);
-    const double t2 = __shfl_down_sync(0xffffffffu, a.t, o);
-    a.join(m2, s2, t2);
-  }
+  warp_join(a.M, a.s, a.t);
   if (WPP > 1) {
     if (lane == 0) {
       sm[w] = a.M;
@@ -267,31 +272,39 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
       st[w] = a.t;
     }
     if (K > 0) {
-      bv[w][lane] = best.v;
-      bi[w][lane] = best.id;
+      // the warps' lists join in pairs
+      for (int r = 1; r < WPP; r *= 2) {
+        if (w % (2 * r) == r) {
+          bv[w][lane] = best.v;
+          bi[w][lane] = best.id;
+        }
+        __syncthreads();
+        if (w % (2 * r) == 0) merge_lists(best, Entry{bv[w + r][lane], bi[w + r][lane]}, lane);
+      }
+    } else {
+      __syncthreads();
     }
-    __syncthreads();
     if (warp != 0) return;
-    if (lane == 0)
-      for (int k = 1; k < WPP; ++k) a.join(sm[k], ss[k], st[k]);
-    if (K > 0)
-      for (int k = 1; k < WPP; ++k) merge_lists(best, Entry{bv[k][lane], bi[k][lane]}, lane);
+    a.M = lane < WPP ? sm[lane] : -INFINITY;
+    a.s = lane < WPP ? ss[lane] : 0.0;
+    a.t = lane < WPP ? st[lane] : 0.0;
+    warp_join(a.M, a.s, a.t);
   }
   const double ls = log(a.s);
   if (lane == 0) {
     if (out.lse != nullptr) out.lse[i] = static_cast<float>(a.M + ls);
     if (out.entropy != nullptr) out.entropy[i] = static_cast<float>(ls - a.t / a.s);
     if (y != nullptr) {
-      const int yi = __ldg(y + i);
+      const int yi = __ldcg(y + i);
       const bool ok = yi >= 0 && yi < V;
       if (!ok) record_status(ctl, kStatusBadTarget);
       // against M before log S: z_y - lse would round away what large logits leave
       if (out.logp != nullptr)
-        out.logp[i] = ok ? static_cast<float>((static_cast<double>(__ldg(zy + i)) - a.M) - ls) : 0.f;
+        out.logp[i] = ok ? static_cast<float>((static_cast<double>(__ldcg(zy + i)) - a.M) - ls) : 0.f;
     }
   }
   if (K > 0) {
-    const double m0 = __shfl_sync(0xffffffffu, a.M, 0), l0 = __shfl_sync(0xffffffffu, ls, 0);
+    const double m0 = a.M, l0 = ls;       // every lane has them
     bool more = lane < K && best.id >= 0;
     int tile = best.id;                   // lane j: the j-th tile
     if (stream && more) {
@@ -302,13 +315,13 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
     const float2* mine = list + static_cast<long long>(tile) * K * ldp + i;
     Entry top{-INFINITY, -1};
     if (more) {
-      const float2 r = __ldg(mine);
+      const float2 r = __ldcg(mine);
       top = Entry{r.x, __float_as_int(r.y)};
     }
     for (int j = 1; j < K; ++j) {
       Entry e{-INFINITY, -1};
       if (more) {
-        const float2 r = __ldg(mine + static_cast<long long>(j) * ldp);
+        const float2 r = __ldcg(mine + static_cast<long long>(j) * ldp);
         if (r.x > kFloor) e = Entry{r.x, __float_as_int(r.y)};
       }
       more = take_entries<K>(top, e, lane);   // a tile's entries fall: no later one can go in either
@@ -434,12 +447,10 @@ cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, 
                          const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
   const uint32_t* tau = with_tau ? b.tau : nullptr;
   if (n <= kWideFinish)
-    k_stats_finish<K, 8><<<n, 256, 0, st>>>(b.part, b.tsum, b.list, tau, b.zy, y, n, S, V, b.ldp,
-                                            stream, out, ctl);
-  else
-    k_stats_finish<K, 1><<<(n + 7) / 8, 256, 0, st>>>(b.part, b.tsum, b.list, tau, b.zy, y, n, S, V,
-                                                      b.ldp, stream, out, ctl);
-  return cudaGetLastError();
+    return launch_after(k_stats_finish<K, 8>, dim3(n), 256, st, b.part, b.tsum, b.list, tau, b.zy, y,
+                        n, S, V, b.ldp, stream, out, ctl);
+  return launch_after(k_stats_finish<K, 1>, dim3((n + 7) / 8), 256, st, b.part, b.tsum, b.list, tau,
+                      b.zy, y, n, S, V, b.ldp, stream, out, ctl);
 }
 
 }  // namespace

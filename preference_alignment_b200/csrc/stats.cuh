@@ -56,6 +56,26 @@ __device__ __forceinline__ void insert_entry(Entry& list, const Entry& x, int la
   else if (lane > at) list = up;
 }
 
+// Joins (M, S, T) of the lanes: every lane gets the warp's.
+__device__ __forceinline__ void warp_join(float& M, double& s, double& t) {
+  float top = M;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (M == -INFINITY) {
+    s = t = 0.0;
+  } else if (M != top) {
+    const double f = expf(M - top);
+    t = f * (t + s * static_cast<double>(M - top));
+    s *= f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    t += __shfl_xor_sync(0xffffffffu, t, o);
+  }
+  M = top;
+}
+
 // Puts every lane's e (id >= 0) into a falling list of which the first K count, as far as it is
 // ahead of the K-th. Returns whether this lane's was when the call began.
 template <int K>

@@ -14,6 +14,7 @@
 // 2-9 turn the accumulator around through shared memory (z[position][vocabulary row]); then each
 // thread has one position and one segment of a tile's rows, keeps the running maximum, S, T and
 // its K largest logits in registers.
+#include "chain.cuh"
 #include "internal.h"
 #include "stats.cuh"
 
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const uint32_t acce0 = smem_u32(bars + 2 * kStages + 2);
   const uint32_t drain = smem_u32(bars + 2 * kStages + 4);
 
+  let_next_start();
   const StreamSplit split(a.V, gridDim.x);
   const int tiles = split.tiles(blockIdx.x);
 
