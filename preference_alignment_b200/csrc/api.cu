@@ -560,15 +560,15 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
     b.ldp = s.ldp;
     int S = stats_tiles(bf16, V);
     const bool stream = bf16 && n <= kStreamMax;   // by the call's n: a chunk never changes the route
+    int stream_rows = 0;
     if (stream) {
-      CUtensorMap mW, mWp, mH;
-      if (!make_map(&mW, W, d, V, 2ull * d, kBK, kStreamRows) ||
-          !make_map(&mWp, W, d, V, 2ull * d, kBK, stats_stream_share(V, di.sms)) ||
+      S = stats_stream_ctas(V, di.sms);
+      stream_rows = stats_stream_rows(V, S);
+      CUtensorMap mW, mH;
+      if (!make_map(&mW, W, d, V, 2ull * d, kBK, stream_rows) ||
           !make_map(&mH, H, d, m, 2ull * h_stride, kBK, stats_stream_cols(m)))
         return DPO_ERR_CUDA;
-      S = stats_stream_ctas(V, std::min(di.sms, kStreamCtas));
-      if (launch_stats_stream(mW, mWp, mH, b, o.n_top, m, V, d, yc, di.sms, ctl, st) !=
-          cudaSuccess)
+      if (launch_stats_stream(mW, mH, b, o.n_top, m, V, d, yc, S, ctl, st) != cudaSuccess)
         return DPO_ERR_CUDA;
     } else if (bf16) {
       CUtensorMap mA, mB;
@@ -585,7 +585,7 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
           cudaSuccess)
         return DPO_ERR_CUDA;
     }
-    if (launch_stats_finish(b, bf16, S, stream, o.n_top, m, V, yc, logp ? logp + i0 : nullptr,
+    if (launch_stats_finish(b, bf16, S, stream_rows, o.n_top, m, V, yc, logp ? logp + i0 : nullptr,
                             o.entropy ? o.entropy + i0 : nullptr,
                             o.lse_state ? o.lse_state + i0 : nullptr,
                             o.n_top ? o.top_ids + i0 * o.n_top : nullptr,

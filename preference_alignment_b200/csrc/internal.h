@@ -159,21 +159,21 @@ cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, 
                              const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
                              cudaStream_t st);
 // The streaming form for up to kStreamMax positions of the bf16 route: one set of partials per CTA.
-// mapW / mapWp: W in boxes of kStreamRows / stats_stream_share rows, mapH: the positions in boxes
-// of stats_stream_cols(n) rows.
+// mapW: W in boxes of stats_stream_rows(V, ctas) rows, mapH: the positions in boxes of
+// stats_stream_cols(n) rows.
 constexpr int kStreamMax = 64;
 constexpr int kStreamCtas = 148;      // CTAs at most, what the workspace has room for
 int stats_stream_cols(int n);
-constexpr int kStreamRows = 128;      // vocabulary rows per tile
+constexpr int kStreamRows = 128;      // vocabulary rows per tile at most
 constexpr int kStreamLists = 4;       // lists per CTA and position
 int stats_stream_ctas(int V, int sms);
-int stats_stream_share(int V, int sms);
-cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapWp,
-                                const CUtensorMap& mapH, const StatsBuf& b, int n_top, int n, int V,
-                                int d, const int* y, int sms, const DevCtl& ctl, cudaStream_t st);
-// Joins S sets of sums (thresholds: those of the bf16 kernels; stream: the streaming form's
-// sums and lists).
-cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, bool stream, int n_top,
+int stats_stream_rows(int V, int ctas);   // vocabulary rows per tile
+cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapH,
+                                const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
+                                int ctas, const DevCtl& ctl, cudaStream_t st);
+// Joins S sets of sums (thresholds: those of the bf16 kernels; stream_rows: the streaming form's
+// sums and lists, its rows per tile; else 0).
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int stream_rows, int n_top,
                                 int n, int V, const int* y,
                                 float* logp, float* entropy, float* lse, int* top_ids,
                                 float* top_logp, const DevCtl& ctl, cudaStream_t st);

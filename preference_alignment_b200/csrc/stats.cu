@@ -180,9 +180,9 @@ struct StatsOut {
 // every tile's list instead, in one chain of dependent loads, took 230 us of the 435 us of a
 // single token at V = 128,256.)
 //
-// stream false: S tiles in id order, each with a sum and (if its maximum reaches the threshold) a list.
-// stream true: the streaming form, S CTAs with a sum each and segs lists each, whose first entries
-// tell their order.
+// stream_rows = 0: S tiles in id order, each with a sum and (if its maximum reaches the threshold)
+// a list. stream_rows > 0: the streaming form with tiles of that many rows, S CTAs with a sum and
+// kSSegs lists each, whose first entries tell their order.
 template <int K, int WPP>
 __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__ part,
                                                       const float* __restrict__ tsum,
@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
                                                       const uint32_t* __restrict__ tau,
                                                       const float* __restrict__ zy,
                                                       const int* __restrict__ y, int n, int S,
-                                                      int V, int ldp, bool stream, StatsOut out, DevCtl ctl) {
+                                                      int V, int ldp, int stream_rows, StatsOut out,
+                                                      DevCtl ctl) {
+  const bool stream = stream_rows > 0;
   constexpr int kJoin = WPP > 1 ? WPP : 1;
   __shared__ float sm[kJoin];
   __shared__ double ss[kJoin], st[kJoin];
@@ -307,11 +309,7 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
     const double m0 = a.M, l0 = ls;       // every lane has them
     bool more = lane < K && best.id >= 0;
     int tile = best.id;                   // lane j: the j-th tile
-    if (stream && more) {
-      int cta, row;
-      StreamSplit(V, S).owner(best.id, cta, row);
-      tile = cta * kSSegs + row / kSegRows;
-    }
+    if (stream && more) tile = StreamSplit{V, S, stream_rows}.list_of(best.id);
     const float2* mine = list + static_cast<long long>(tile) * K * ldp + i;
     Entry top{-INFINITY, -1};
     if (more) {
@@ -442,15 +440,15 @@ cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const S
 }
 
 template <int K>
-cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, bool stream,
+cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, int stream_rows,
                          const int* y,
                          const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
   const uint32_t* tau = with_tau ? b.tau : nullptr;
   if (n <= kWideFinish)
     return launch_after(k_stats_finish<K, 8>, dim3(n), 256, st, b.part, b.tsum, b.list, tau, b.zy, y,
-                        n, S, V, b.ldp, stream, out, ctl);
+                        n, S, V, b.ldp, stream_rows, out, ctl);
   return launch_after(k_stats_finish<K, 1>, dim3((n + 7) / 8), 256, st, b.part, b.tsum, b.list, tau,
-                      b.zy, y, n, S, V, b.ldp, stream, out, ctl);
+                      b.zy, y, n, S, V, b.ldp, stream_rows, out, ctl);
 }
 
 }  // namespace
@@ -481,11 +479,11 @@ cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, bool stream, int n_top,
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int stream_rows, int n_top,
                                 int n, int V, const int* y, float* logp, float* entropy, float* lse, int* top_ids,
                                 float* top_logp, const DevCtl& ctl, cudaStream_t st) {
   const StatsOut out{logp, entropy, lse, top_logp, top_ids, n_top};
-  return DPO_BY_LIST(stats_list_len(n_top), stats_finish)(b, thresholds, n, S, V, stream, y, out, ctl,
+  return DPO_BY_LIST(stats_list_len(n_top), stats_finish)(b, thresholds, n, S, V, stream_rows, y, out, ctl,
                                                           st);
 }
 

@@ -139,46 +139,23 @@ __device__ __forceinline__ void insert_sorted(float (&val)[K], int (&id)[K], flo
 }
 
 // ------------------------------------------------------------------ the streaming form's split
-constexpr int kSRows = kStreamRows;
-constexpr int kSPiece = 8;       // rows the short tiles are cut at
+constexpr int kSRows = kStreamRows;    // rows a tile has room for: the accumulator's lanes
+constexpr int kSWarps = 8;             // warps that take positions
 constexpr int kSSegs = kStreamLists;   // threads per position, and a thread's rows of a tile
 constexpr int kSegRows = kSRows / kSSegs;
-constexpr int kSWarps = 8;       // warps that take positions
 
-// Which vocabulary rows a CTA takes: whole tiles side by side, then its share of the rest in
-// pieces of kSPiece rows.
+// Tile t of `rows` vocabulary rows goes to CTA t mod ctas; rows is what makes all CTAs' tiles
+// equal (stats_stream_rows).
 struct StreamSplit {
-  int V, ctas, waves, rest0, pieces;      // rest0: first row after the whole waves
-  __device__ __forceinline__ StreamSplit(int V_, int ctas_) : V(V_), ctas(ctas_) {
-    waves = V / (kSRows * ctas);
-    rest0 = waves * kSRows * ctas;
-    pieces = (V - rest0 + kSPiece - 1) / kSPiece;
-  }
-  __device__ __forceinline__ int rest(int cta) const {       // first row of the CTA's share
-    return rest0 + static_cast<int>(static_cast<long long>(pieces) * cta / ctas) * kSPiece;
-  }
+  int V, ctas, rows;
   __device__ __forceinline__ int tiles(int cta) const {
-    return waves + (rest(cta + 1) > rest(cta) ? 1 : 0);
+    const int all = (V + rows - 1) / rows;
+    return cta < all ? (all - cta + ctas - 1) / ctas : 0;
   }
-  __device__ __forceinline__ void tile(int cta, int t, int& r0, int& rows) const {
-    if (t < waves) {
-      r0 = (t * ctas + cta) * kSRows;
-      rows = kSRows;
-    } else {
-      r0 = rest(cta);
-      rows = min(V, rest(cta + 1)) - r0;
-    }
-  }
-  // The CTA and the row within its tile that vocabulary row v went to.
-  __device__ __forceinline__ void owner(int v, int& cta, int& row) const {
-    if (v < rest0) {
-      cta = v / kSRows % ctas;
-      row = v % kSRows;
-    } else {
-      const long long q = (v - rest0) / kSPiece;             // the last cta with rest(cta) <= v
-      cta = static_cast<int>(((q + 1) * ctas - 1) / pieces);
-      row = v - rest(cta);
-    }
+  __device__ __forceinline__ int first(int cta, int t) const { return (t * ctas + cta) * rows; }
+  // The list of vocabulary row v: its CTA's, of the segment its row of the tile falls into.
+  __device__ __forceinline__ int list_of(int v) const {
+    return v / rows % ctas * kSSegs + v % rows / kSegRows;
   }
 };
 

@@ -4,16 +4,18 @@
 // Orientation: W rows are the accumulator's 128 lanes and the NT positions its columns, z^T = W .
 // Hp^T, so a pipeline stage is 16 KiB of W and only NT * 128 bytes of hidden rows (the other
 // orientation pads a few positions to 128 rows, 16 KiB a stage). The CTAs walk W side by side,
-// tile t of 128 rows going to CTA t mod gridDim, and what does not fill a last wave is cut into
-// equal pieces: a short last tile each, whose missing rows are not loaded. (One contiguous range
-// per CTA reads 148 places of W at a time instead of one: 187 us instead of 164 us at V = 128,256,
-// d = 4096.) Every running value stays on chip until the CTA is done, so a position leaves one set
+// tile t going to CTA t mod gridDim, in tiles of at most 128 rows so many that every CTA gets the
+// same number (V = 151,936: 9 tiles of 115 rows on each of 148 CTAs; with 128 rows, 3 tiles would
+// make a ninth wave). (One contiguous range per CTA reads 148 places of W at a time instead of
+// one: 187 us instead of 164 us at V = 128,256, d = 4096.) Every running value stays on chip until the CTA is done, so a position leaves one set
 // of sums per CTA, not one per tile.
 //
 // Roles (320 threads): warp 0 issues the TMA loads, warp 1 owns TMEM and issues the MMAs, warps
 // 2-9 turn the accumulator around through shared memory (z[position][vocabulary row]); then each
 // thread has one position and one segment of a tile's rows, keeps the running maximum, S, T and
 // its K largest logits in registers.
+#include <algorithm>
+
 #include "chain.cuh"
 #include "internal.h"
 #include "stats.cuh"
@@ -88,13 +90,12 @@ struct StreamArgs {
   uint32_t* tau;        // [K groups, ldp] thresholds, zeroed before the launch
   float2* list;         // [gridDim.x * kSSegs, K, ldp]
   int n, V, k_blocks, ldp;
-  int share;            // rows of tmWp's boxes: the largest share of what the whole waves leave
+  int rows;             // vocabulary rows per tile
 };
 
 template <int NT, int K>
 __global__ void __launch_bounds__(kSThreads, 1)
     k_stats_stream(const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmWp,
                    const __grid_constant__ CUtensorMap tmH, StreamArgs a, DevCtl ctl) {
   using Sh = StreamShape<NT>;
   constexpr int kStages = Sh::kStages;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const uint32_t drain = smem_u32(bars + 2 * kStages + 4);
 
   let_next_start();
-  const StreamSplit split(a.V, gridDim.x);
+  const StreamSplit split{a.V, static_cast<int>(gridDim.x), a.rows};
   const int tiles = split.tiles(blockIdx.x);
 
   if (threadIdx.x == 0) {
@@ -136,7 +137,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmWp);
     tma_prefetch_desc(&tmH);
   }
   if (warp == 1) {
@@ -158,10 +158,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int t = 0; t < tiles && ok; ++t) {
-      int r0, rows;
-      split.tile(blockIdx.x, t, r0, rows);
-      const bool whole = t < split.waves;
-      const uint32_t bytes = (whole ? kSRows : a.share) * kBK * 2 + Sh::kHBytes;
+      const int r0 = split.first(blockIdx.x, t);
+      const uint32_t bytes = a.rows * kBK * 2 + Sh::kHBytes;   // rows past V arrive as zeros
       for (int kb = 0; kb < a.k_blocks; ++kb) {
         if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, ctl, abort_flag)) {
           ok = false;
@@ -170,7 +168,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         const uint32_t fb = full0 + 8 * stage;
         mbar_arrive_expect_tx(fb, bytes);
         const uint32_t w_dst = smem_u32(sW + stage * kSWBytes);
-        tma_load_2d(w_dst, whole ? &tmW : &tmWp, fb, kb * kBK, r0);
+        tma_load_2d(w_dst, &tmW, fb, kb * kBK, r0);
         tma_load_2d(smem_u32(sH + stage * Sh::kHBytes), &tmH, fb, kb * kBK, 0);
         issued_mask |= 1u << stage;
         issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
@@ -276,8 +274,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
           z[(c0 + c) * kPitch + quad * 32 + lane] = __uint_as_float(v[c]);
       }
       warps_sync();
-      int r0, rows;
-      split.tile(blockIdx.x, t, r0, rows);
+      const int r0 = split.first(blockIdx.x, t);
+      const int rows = min(a.rows, a.V - r0);
       const float* zp = z + p * kPitch + (seg % kSSegs) * kSegRows;
       float x[kSegRows];
       float cm = -INFINITY;
@@ -343,10 +341,22 @@ __global__ void __launch_bounds__(kSThreads, 1)
         a.tsum[to] = static_cast<float>(j.t);
       }
       if (K > 0 && mine) {
-        float2* l = a.list + static_cast<long long>(set) * kList * a.ldp + p;
+        // the finish reads no further than the first entry below the threshold
+        uint32_t th = 0xffffffffu;
 #pragma unroll
-        for (int j = 0; j < kList; ++j)
-          l[static_cast<long long>(j) * a.ldp] = make_float2(val[j], __int_as_float(id[j]));
+        for (int g = 0; g < kList; ++g)
+          th = min(th, __ldcg(a.tau + static_cast<long long>(g) * a.ldp + p));
+        const float tauv = from_ordered(th);
+        float2* l = a.list + static_cast<long long>(set) * kList * a.ldp + p;
+        bool open = true;
+#pragma unroll
+        for (int j = 0; j < kList; ++j) {
+          const bool keep = val[j] > kFloor && val[j] >= tauv;
+          if (open)
+            l[static_cast<long long>(j) * a.ldp] =
+                keep ? make_float2(val[j], __int_as_float(id[j])) : make_float2(kFloor, 0.f);
+          open = keep;
+        }
       }
     }
   }
@@ -371,24 +381,24 @@ __global__ void __launch_bounds__(kSThreads, 1)
 }
 
 template <int NT, int K>
-cudaError_t stream_launch(const CUtensorMap& mW, const CUtensorMap& mWp, const CUtensorMap& mH,
-                          const StreamArgs& a, int grid, const DevCtl& ctl, cudaStream_t st) {
+cudaError_t stream_launch(const CUtensorMap& mW, const CUtensorMap& mH, const StreamArgs& a,
+                          int grid, const DevCtl& ctl, cudaStream_t st) {
   auto kern = k_stats_stream<NT, K>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              StreamShape<NT>::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kSThreads, StreamShape<NT>::kSmem, st>>>(mW, mWp, mH, a, ctl);
+  kern<<<grid, kSThreads, StreamShape<NT>::kSmem, st>>>(mW, mH, a, ctl);
   return cudaGetLastError();
 }
 
 template <int K>
-cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mWp,
-                                const CUtensorMap& mH, const StreamArgs& a, int grid,
+cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mH,
+                                const StreamArgs& a, int grid,
                                 const DevCtl& ctl, cudaStream_t st) {
   switch (stats_stream_cols(a.n)) {
-    case 16: return stream_launch<16, K>(mW, mWp, mH, a, grid, ctl, st);
-    case 32: return stream_launch<32, K>(mW, mWp, mH, a, grid, ctl, st);
-    default: return stream_launch<64, K>(mW, mWp, mH, a, grid, ctl, st);
+    case 16: return stream_launch<16, K>(mW, mH, a, grid, ctl, st);
+    case 32: return stream_launch<32, K>(mW, mH, a, grid, ctl, st);
+    default: return stream_launch<64, K>(mW, mH, a, grid, ctl, st);
   }
 }
 
@@ -396,22 +406,19 @@ cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mWp,
 
 int stats_stream_cols(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : 64; }
 
+// One CTA per SM, of 8 rows at least.
 int stats_stream_ctas(int V, int sms) {
-  const int pieces = (V + kSPiece - 1) / kSPiece;
-  return pieces < sms ? pieces : sms;
+  return std::min(std::min(sms, kStreamCtas), (V + 7) / 8);
 }
 
-int stats_stream_share(int V, int sms) {
-  const int ctas = stats_stream_ctas(V, sms < kStreamCtas ? sms : kStreamCtas);
-  const int rest = V - V / (kSRows * ctas) * kSRows * ctas;
-  const int pieces = (rest + kSPiece - 1) / kSPiece;
-  const int share = (pieces + ctas - 1) / ctas;
-  return (share > 0 ? share : 1) * kSPiece;
+int stats_stream_rows(int V, int ctas) {
+  const int tiles = (V + kSRows * ctas - 1) / (kSRows * ctas);      // per CTA
+  return (V + ctas * tiles - 1) / (ctas * tiles);
 }
 
-cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapWp,
-                                const CUtensorMap& mapH, const StatsBuf& b, int n_top, int n, int V,
-                                int d, const int* y, int sms, const DevCtl& ctl, cudaStream_t st) {
+cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapH,
+                                const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
+                                int ctas, const DevCtl& ctl, cudaStream_t st) {
   const int K = stats_list_len(n_top);
   if (K > 0) {
     const cudaError_t e =
@@ -419,13 +426,12 @@ cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapW
     if (e != cudaSuccess) return e;
   }
   const StreamArgs a{y, b.part, b.tsum, b.zy, b.tau, b.list, n, V, (d + kBK - 1) / kBK, b.ldp,
-                     stats_stream_share(V, sms)};
-  const int grid = stats_stream_ctas(V, sms < kStreamCtas ? sms : kStreamCtas);
+                     stats_stream_rows(V, ctas)};
   switch (K) {
-    case 0: return stream_by_positions<0>(mapW, mapWp, mapH, a, grid, ctl, st);
-    case 1: return stream_by_positions<1>(mapW, mapWp, mapH, a, grid, ctl, st);
-    case 8: return stream_by_positions<8>(mapW, mapWp, mapH, a, grid, ctl, st);
-    default: return stream_by_positions<32>(mapW, mapWp, mapH, a, grid, ctl, st);
+    case 0: return stream_by_positions<0>(mapW, mapH, a, ctas, ctl, st);
+    case 1: return stream_by_positions<1>(mapW, mapH, a, ctas, ctl, st);
+    case 8: return stream_by_positions<8>(mapW, mapH, a, ctas, ctl, st);
+    default: return stream_by_positions<32>(mapW, mapH, a, ctas, ctl, st);
   }
 }
 
