@@ -494,12 +494,7 @@ StatsPlan stats_layout(size_t prefix, long long n_lp, long long n, int V, bool b
                        int chunk) {
   StatsPlan s;
   s.chunk = chunk;
-  const size_t ctas = stats_stream_ctas(V, kStreamCtas);
-  const bool stream = bf16 && n <= kStreamMax;
-  const size_t tiles = stream ? ctas : stats_tiles(bf16, V);
-  const size_t lists = stream ? ctas * kStreamLists : tiles;
-  const size_t ldp = stream ? n : align_up(chunk > 0 ? chunk : 1, 32);
-  s.ldp = static_cast<int>(ldp);
+  const size_t K = stats_list_len(n_top);
   size_t o = prefix;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -507,11 +502,21 @@ StatsPlan stats_layout(size_t prefix, long long n_lp, long long n, int V, bool b
     return at;
   };
   s.off_lp = take(sizeof(float) * static_cast<size_t>(n_lp));
-  s.off_part = take(sizeof(float2) * tiles * ldp);
-  s.off_tsum = take(sizeof(float) * tiles * ldp);
-  s.off_zy = take(sizeof(float) * ldp);
-  s.off_tau = take(sizeof(uint32_t) * ldp * stats_list_len(n_top));
-  s.off_list = take(sizeof(float2) * lists * ldp * stats_list_len(n_top));
+  if (bf16 && n <= kStreamMax) {
+    const size_t sets = static_cast<size_t>(n) * stats_stream_ctas(V, kStreamCtas);
+    s.off_part = take(sizeof(float4) * sets);
+    s.off_zy = take(sizeof(float) * static_cast<size_t>(n));
+    s.off_list = take(sizeof(float2) * sets * kStreamLists * K);
+  } else {
+    const size_t tiles = stats_tiles(bf16, V);
+    const size_t ldp = align_up(chunk > 0 ? chunk : 1, 32);
+    s.ldp = static_cast<int>(ldp);
+    s.off_part = take(sizeof(float2) * tiles * ldp);
+    s.off_tsum = take(sizeof(float) * tiles * ldp);
+    s.off_zy = take(sizeof(float) * ldp);
+    s.off_tau = take(sizeof(uint32_t) * ldp * K);
+    s.off_list = take(sizeof(float2) * tiles * ldp * K);
+  }
   s.total = o;
   return s;
 }
@@ -558,19 +563,22 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
     b.tau = reinterpret_cast<uint32_t*>(w + s.off_tau);
     b.list = reinterpret_cast<float2*>(w + s.off_list);
     b.ldp = s.ldp;
-    int S = stats_tiles(bf16, V);
-    const bool stream = bf16 && n <= kStreamMax;   // by the call's n: a chunk never changes the route
-    int stream_rows = 0;
-    if (stream) {
-      S = stats_stream_ctas(V, di.sms);
-      stream_rows = stats_stream_rows(V, S);
+    const StatsOut out{logp ? logp + i0 : nullptr, o.entropy ? o.entropy + i0 : nullptr,
+                       o.lse_state ? o.lse_state + i0 : nullptr,
+                       o.n_top ? o.top_logp + i0 * o.n_top : nullptr,
+                       o.n_top ? o.top_ids + i0 * o.n_top : nullptr, o.n_top};
+    // by the call's n: a chunk never changes the route
+    if (bf16 && n <= kStreamMax) {
+      const int ctas = stats_stream_ctas(V, di.sms);
       CUtensorMap mW, mH;
-      if (!make_map(&mW, W, d, V, 2ull * d, kBK, stream_rows) ||
+      if (!make_map(&mW, W, d, V, 2ull * d, kBK, stats_stream_rows(V, ctas)) ||
           !make_map(&mH, H, d, m, 2ull * h_stride, kBK, stats_stream_cols(m)))
         return DPO_ERR_CUDA;
-      if (launch_stats_stream(mW, mH, b, o.n_top, m, V, d, yc, S, ctl, st) != cudaSuccess)
+      if (launch_stats_stream(mW, mH, b, out, m, V, d, yc, ctas, ctl, st) != cudaSuccess)
         return DPO_ERR_CUDA;
-    } else if (bf16) {
+      continue;
+    }
+    if (bf16) {
       CUtensorMap mA, mB;
       if (!make_map(&mA, static_cast<const uint16_t*>(H) + i0 * h_stride, d, m, 2ull * h_stride,
                     kBK, kBoxRows) ||
@@ -585,11 +593,7 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
           cudaSuccess)
         return DPO_ERR_CUDA;
     }
-    if (launch_stats_finish(b, bf16, S, stream_rows, o.n_top, m, V, yc, logp ? logp + i0 : nullptr,
-                            o.entropy ? o.entropy + i0 : nullptr,
-                            o.lse_state ? o.lse_state + i0 : nullptr,
-                            o.n_top ? o.top_ids + i0 * o.n_top : nullptr,
-                            o.n_top ? o.top_logp + i0 * o.n_top : nullptr, ctl, st) != cudaSuccess)
+    if (launch_stats_finish(b, bf16, stats_tiles(bf16, V), m, V, yc, out, ctl, st) != cudaSuccess)
       return DPO_ERR_CUDA;
   }
   return DPO_OK;

@@ -149,6 +149,12 @@ struct StatsBuf {
   float2* list;      // [S, stats_list_len, ldp]
   int ldp;
 };
+// Where the results of a chunk go (any pointer may be NULL; n_top alternatives per position).
+struct StatsOut {
+  float *logp, *entropy, *lse, *top_logp;
+  int* top_ids;
+  int n_top;
+};
 int stats_list_len(int n_top);               // entries kept per tile for n_top alternatives
 int stats_tiles(bool bf16, int V);
 cudaError_t launch_stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const StatsBuf& b,
@@ -158,7 +164,8 @@ cudaError_t launch_stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, 
 cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, const float* W,
                              const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
                              cudaStream_t st);
-// The streaming form for up to kStreamMax positions of the bf16 route: one set of partials per CTA.
+// The streaming form for up to kStreamMax positions of the bf16 route, its join included: one set
+// of sums (16 bytes at b.part) and kStreamLists lists (b.list) per CTA and position.
 // mapW: W in boxes of stats_stream_rows(V, ctas) rows, mapH: the positions in boxes of
 // stats_stream_cols(n) rows.
 constexpr int kStreamMax = 64;
@@ -169,14 +176,12 @@ constexpr int kStreamLists = 4;       // lists per CTA and position
 int stats_stream_ctas(int V, int sms);
 int stats_stream_rows(int V, int ctas);   // vocabulary rows per tile
 cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapH,
-                                const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
-                                int ctas, const DevCtl& ctl, cudaStream_t st);
-// Joins S sets of sums (thresholds: those of the bf16 kernels; stream_rows: the streaming form's
-// sums and lists, its rows per tile; else 0).
-cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int stream_rows, int n_top,
-                                int n, int V, const int* y,
-                                float* logp, float* entropy, float* lse, int* top_ids,
-                                float* top_logp, const DevCtl& ctl, cudaStream_t st);
+                                const StatsBuf& b, const StatsOut& out, int n, int V, int d,
+                                const int* y, int ctas, const DevCtl& ctl, cudaStream_t st);
+// Joins the S tiles of the GEMM's or the SIMT route's partials (thresholds: the GEMM's).
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int n, int V,
+                                const int* y, const StatsOut& out, const DevCtl& ctl,
+                                cudaStream_t st);
 
 // 8-bit activation checkpoints (checkpoint.cu) and the norm before the head (norm.cu).
 cudaError_t launch_ckpt_pack(bool bf16, int rows, int d, const void* x, long long stride,

@@ -61,7 +61,6 @@ __global__ void __launch_bounds__(kShortThreads) k_norm_bwd_short(X x, Dy dy, Dx
 #pragma unroll
   for (int j = 0; j < 4; ++j) w[j] = aw[j] = ab[j] = both(0.f);
   if (in) load_vec(a.weight, a.wbf16, col, 1.f, w);
-  let_next_start();
   // every thread of a warp makes the same number of rounds: the exchanges need them all
   const long long step = static_cast<long long>(gridDim.x) * kRows;
   const long long first = static_cast<long long>(blockIdx.x) * kRows;
@@ -147,7 +146,6 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
     }
     cp_async_commit();
   };
-  let_next_start();
   fetch(row, ring);
   fetch(row + step, ring + kSlot);
   // the next row's statistics and scales are asked for while this one is worked on

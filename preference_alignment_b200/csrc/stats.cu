@@ -164,12 +164,6 @@ struct EpiStats {
 };
 
 // ------------------------------------------------------------------ finish
-struct StatsOut {
-  float *logp, *entropy, *lse, *top_logp;
-  int* top_ids;
-  int n_top;
-};
-
 // WPP warps per position (the block's 8 warps hold 8 / WPP positions): lane l of warp w joins
 // tiles 32 w + l, 32 w + l + 32 WPP, ..., then lanes and warps join in a fixed order.
 //
@@ -179,10 +173,6 @@ struct StatsOut {
 // the tiles' second, third, ... entries go in until none is ahead of the list's last. (Joining
 // every tile's list instead, in one chain of dependent loads, took 230 us of the 435 us of a
 // single token at V = 128,256.)
-//
-// stream_rows = 0: S tiles in id order, each with a sum and (if its maximum reaches the threshold)
-// a list. stream_rows > 0: the streaming form with tiles of that many rows, S CTAs with a sum and
-// kSSegs lists each, whose first entries tell their order.
 template <int K, int WPP>
 __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__ part,
                                                       const float* __restrict__ tsum,
@@ -190,9 +180,7 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
                                                       const uint32_t* __restrict__ tau,
                                                       const float* __restrict__ zy,
                                                       const int* __restrict__ y, int n, int S,
-                                                      int V, int ldp, int stream_rows, StatsOut out,
-                                                      DevCtl ctl) {
-  const bool stream = stream_rows > 0;
+                                                      int V, int ldp, StatsOut out, DevCtl ctl) {
   constexpr int kJoin = WPP > 1 ? WPP : 1;
   __shared__ float sm[kJoin];
   __shared__ double ss[kJoin], st[kJoin];
@@ -205,20 +193,6 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
   after_previous();
   // what the kernel before wrote is read past L1 (__ldcg): this one may have started before it
   constexpr int U = 4;
-  Entry first[U];                         // the streaming form's sets, asked for before the sums
-  const int sets = stream ? S * kSSegs : 0;
-  auto load_sets = [&](int base) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = base + (u * WPP + w) * 32 + lane;
-      first[u] = Entry{-INFINITY, -1};
-      if (k < sets) {
-        const float2 r = __ldcg(list + static_cast<long long>(k) * K * ldp + i);
-        if (r.x > kFloor) first[u] = Entry{r.x, __float_as_int(r.y)};
-      }
-    }
-  };
-  if (K > 0 && stream) load_sets(0);
   uint32_t th = 0;
   if (K > 0 && tau != nullptr)
     th = lane < K ? __ldcg(tau + static_cast<long long>(lane) * ldp + i) : 0xffffffffu;
@@ -242,7 +216,7 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       a.join(q[u].x, q[u].y, tq[u]);
-      if (K > 0 && !stream) {
+      if (K > 0) {
         // tiles come in rising order: an equal maximum is behind the ones held
         const float m = q[u].x > kFloor && q[u].x >= tauv ? q[u].x : -INFINITY;
         uint32_t hit = __ballot_sync(0xffffffffu, m > __shfl_sync(0xffffffffu, best.v, K - 1));
@@ -253,16 +227,6 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
           hit &= hit - 1;
           hit &= __ballot_sync(0xffffffffu, m > __shfl_sync(0xffffffffu, best.v, K - 1));
         }
-      }
-    }
-  }
-  if (K > 0 && stream) {
-    for (int base = 0; base < sets; base += 32 * WPP * U) {
-      if (base > 0) load_sets(base);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (first[u].v < tauv) first[u].id = -1;
-        take_entries<K>(best, first[u], lane);
       }
     }
   }
@@ -308,9 +272,7 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
   if (K > 0) {
     const double m0 = a.M, l0 = ls;       // every lane has them
     bool more = lane < K && best.id >= 0;
-    int tile = best.id;                   // lane j: the j-th tile
-    if (stream && more) tile = StreamSplit{V, S, stream_rows}.list_of(best.id);
-    const float2* mine = list + static_cast<long long>(tile) * K * ldp + i;
+    const float2* mine = list + static_cast<long long>(best.id) * K * ldp + i;   // lane j: tile j
     Entry top{-INFINITY, -1};
     if (more) {
       const float2 r = __ldcg(mine);
@@ -440,15 +402,15 @@ cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const S
 }
 
 template <int K>
-cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, int stream_rows,
-                         const int* y,
+cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, const int* y,
+                        
                          const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
   const uint32_t* tau = with_tau ? b.tau : nullptr;
   if (n <= kWideFinish)
     return launch_after(k_stats_finish<K, 8>, dim3(n), 256, st, b.part, b.tsum, b.list, tau, b.zy, y,
-                        n, S, V, b.ldp, stream_rows, out, ctl);
+                        n, S, V, b.ldp, out, ctl);
   return launch_after(k_stats_finish<K, 1>, dim3((n + 7) / 8), 256, st, b.part, b.tsum, b.list, tau,
-                      b.zy, y, n, S, V, b.ldp, stream_rows, out, ctl);
+                      b.zy, y, n, S, V, b.ldp, out, ctl);
 }
 
 }  // namespace
@@ -479,12 +441,10 @@ cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int stream_rows, int n_top,
-                                int n, int V, const int* y, float* logp, float* entropy, float* lse, int* top_ids,
-                                float* top_logp, const DevCtl& ctl, cudaStream_t st) {
-  const StatsOut out{logp, entropy, lse, top_logp, top_ids, n_top};
-  return DPO_BY_LIST(stats_list_len(n_top), stats_finish)(b, thresholds, n, S, V, stream_rows, y, out, ctl,
-                                                          st);
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int n, int V,
+                                const int* y, const StatsOut& out, const DevCtl& ctl,
+                                cudaStream_t st) {
+  return DPO_BY_LIST(stats_list_len(out.n_top), stats_finish)(b, thresholds, n, S, V, y, out, ctl, st);
 }
 
 }  // namespace dpo

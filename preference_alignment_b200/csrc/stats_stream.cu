@@ -35,7 +35,7 @@ struct StreamShape {
   static constexpr int kPitch = kSRows + 1;                // of z: odd, so columns spread over banks
   static constexpr int kZ = NT * kPitch * 4;               // z[position][row], later the sums
   static constexpr int kSmem =
-      kStages * kStage + kZ + NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
+      kStages * kStage + kZ + NT * 4 + kSSegs * NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
   static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -82,14 +82,20 @@ __device__ __forceinline__ bool warps_all(bool mine) {
   return all != 0;
 }
 
+constexpr int kFinish = 256;    // threads of the finish: a block per position
+// Further list entries the finish looks at together, one per thread for each of the K lists.
+__host__ __device__ constexpr int list_batch(int K) {
+  return K <= 1 ? 0 : K * (K - 1) <= kFinish ? K - 1 : kFinish / K;
+}
+
 struct StreamArgs {
   const int* y;         // given tokens, or nullptr
-  float2* part;         // [gridDim.x, ldp]
-  float* tsum;          // [gridDim.x, ldp]
-  float* zy;            // [ldp]
-  uint32_t* tau;        // [K groups, ldp] thresholds, zeroed before the launch
-  float2* list;         // [gridDim.x * kSSegs, K, ldp]
-  int n, V, k_blocks, ldp;
+  // by position, so that the finish reads whole lines
+  float4* part;         // [n, CTAs] (m, S, T, -)
+  float* zy;            // [n]
+  float2* top;          // [n, CTAs * kSSegs] the lists' first entries (logit, id)
+  float2* rest;         // [n, CTAs * kSSegs, K - 1] and the others
+  int n, V, k_blocks;
   int rows;             // vocabulary rows per tile
 };
 
@@ -100,6 +106,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   using Sh = StreamShape<NT>;
   constexpr int kStages = Sh::kStages;
   constexpr int kList = K > 0 ? K : 1;
+  constexpr int kBatch = list_batch(K);
   constexpr int kPitch = Sh::kPitch;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -108,7 +115,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
   uint8_t* sH = sW + kStages * kSWBytes;
   float* z = reinterpret_cast<float*>(sH + kStages * Sh::kHBytes);
   int* sy = reinterpret_cast<int*>(z + NT * Sh::kPitch);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sy + NT);
+  float* share = reinterpret_cast<float*>(sy + NT);    // [kSSegs][NT]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(share + kSSegs * NT);
   // bars: [0, S) full, [S, 2S) empty, 2S + {0,1} acc_full, 2S + {2,3} acc_empty, 2S + 4 drain
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -120,7 +128,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const uint32_t acce0 = smem_u32(bars + 2 * kStages + 2);
   const uint32_t drain = smem_u32(bars + 2 * kStages + 4);
 
-  let_next_start();
   const StreamSplit split{a.V, static_cast<int>(gridDim.x), a.rows};
   const int tiles = split.tiles(blockIdx.x);
 
@@ -243,16 +250,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
     }
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
-      // the groups' thresholds: asked for before the wait for the tile
-      uint32_t th = 0xffffffffu, bid = 0;
-      if (K > 0 && mine) {
-#pragma unroll
-        for (int g = 0; g < kList; ++g) {
-          const uint32_t o = __ldcg(a.tau + static_cast<long long>(g) * a.ldp + p);
-          th = min(th, o);
-          if (g == set % kList) bid = o;
-        }
-      }
       const int acc = t & 1;
       ok = mbar_wait(accf0 + 8 * acc, (t >> 1) & 1, ctl, abort_flag);
       // also: every warp is done with the last tile's z
@@ -301,23 +298,27 @@ __global__ void __launch_bounds__(kSThreads, 1)
         tt = fmaf(ex, fmaxf(b, -1e30f), tt);               // the bound keeps 0 * -inf out of T
       }
       if (K > 0) {
-        const float tauv = from_ordered(th);
-        uint32_t hit = 0;
-        if (mine && cm >= tauv && cm > val[kList - 1]) {
+        // K / 4 logits of each of the position's 4 threads are K logits: one below the smallest of
+        // their (K / 4)-th is no alternative (nor one equal to it: its id would be the highest)
+        float low = val[kList - 1];
+        if (K >= kSSegs && t > 0 && mine) {
+          float all = share[p];
 #pragma unroll
-          for (int j = 0; j < kSegRows; ++j)
-            hit |= (x[j] >= tauv && x[j] > val[kList - 1] ? 1u : 0u) << j;
+          for (int g = 1; g < kSSegs; ++g) all = fminf(all, share[g * NT + p]);
+          low = fmaxf(low, all);
         }
-        if (__any_sync(0xffffffffu, hit != 0)) {
-          while (hit != 0) {
-            const int j = __ffs(hit) - 1;
-            hit &= hit - 1;
-            insert_sorted<kList>(val, id, zp[j], r0 + seg * kSegRows + j);
-          }
-          // the set's largest logit is its group's bid for the threshold
-          if (mine && ordered(val[0]) > bid && val[0] > kFloor)
-            atomicMax(a.tau + static_cast<long long>(set % kList) * a.ldp + p, ordered(val[0]));
+        uint32_t hit = 0;
+        if (mine && cm > low) {
+#pragma unroll
+          for (int j = 0; j < kSegRows; ++j) hit |= (x[j] > low ? 1u : 0u) << j;
         }
+        while (hit != 0) {
+          const int j = __ffs(hit) - 1;
+          hit &= hit - 1;
+          insert_sorted<kList>(val, id, zp[j], r0 + seg * kSegRows + j);
+        }
+        // read after the next tile's barrier
+        if (K >= kSSegs && mine) share[seg * NT + p] = val[kList >= kSSegs ? kList / kSSegs - 1 : 0];
       }
     }
     // a position's segments join in a fixed order, in z's place; one set of sums per CTA
@@ -336,26 +337,27 @@ __global__ void __launch_bounds__(kSThreads, 1)
           const float* w = z + (g * NT + p) * 3;
           j.join(w[0], w[1], w[2]);
         }
-        const long long to = static_cast<long long>(blockIdx.x) * a.ldp + p;
-        a.part[to] = make_float2(j.M, static_cast<float>(j.s));
-        a.tsum[to] = static_cast<float>(j.t);
+        a.part[static_cast<long long>(p) * gridDim.x + blockIdx.x] =
+            make_float4(j.M, static_cast<float>(j.s), static_cast<float>(j.t), 0.f);
       }
       if (K > 0 && mine) {
-        // the finish reads no further than the first entry below the threshold
-        uint32_t th = 0xffffffffu;
+        const long long at = static_cast<long long>(p) * gridDim.x * kSSegs + set;
+        a.top[at] = make_float2(val[0], __int_as_float(id[0]));
+        // entries that K others are ahead of are left out: the finish reads a batch at a time and
+        // goes on to the next only from a full one
+        float low = kFloor;
+        if (K >= kSSegs) {
+          low = share[p];
 #pragma unroll
-        for (int g = 0; g < kList; ++g)
-          th = min(th, __ldcg(a.tau + static_cast<long long>(g) * a.ldp + p));
-        const float tauv = from_ordered(th);
-        float2* l = a.list + static_cast<long long>(set) * kList * a.ldp + p;
+          for (int g = 1; g < kSSegs; ++g) low = fminf(low, share[g * NT + p]);
+        }
+        float2* l = a.rest + at * (kList - 1);
         bool open = true;
 #pragma unroll
-        for (int j = 0; j < kList; ++j) {
-          const bool keep = val[j] > kFloor && val[j] >= tauv;
-          if (open)
-            l[static_cast<long long>(j) * a.ldp] =
-                keep ? make_float2(val[j], __int_as_float(id[j])) : make_float2(kFloor, 0.f);
-          open = keep;
+        for (int j = 1; j < kList; ++j) {
+          const bool keep = val[j] > kFloor && val[j] >= low;
+          if (open) l[j - 1] = keep ? make_float2(val[j], __int_as_float(id[j])) : make_float2(kFloor, 0.f);
+          if (j % (kBatch > 0 ? kBatch : 1) == 0) open = keep;
         }
       }
     }
@@ -380,6 +382,149 @@ __global__ void __launch_bounds__(kSThreads, 1)
   }
 }
 
+// One block per position joins the CTAs' sums and lists.
+//
+// Alternatives, all without a chain of insertions: (1) the first entries of the lists, dealt out
+// over K groups, give K different logits, the groups' maxima, so the smallest of those is a lower
+// bound of the K-th largest first entry, which about K log K of them reach; (2) each of these
+// counts how many are ahead of it, its rank: the K first are the lists that can hold any of the K
+// largest logits; (3) the further entries of those lists that are ahead of the K-th so far join
+// them, and their ranks are the answer. (Inserting one by one in a warp took 12 us instead of 5
+// us at K = 8.)
+constexpr int kStreamSets = kStreamCtas * kSSegs;
+
+template <int K>
+__global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, int ctas,
+                                                                 StatsOut out, DevCtl ctl) {
+  constexpr int kList = K > 0 ? K : 1;
+  constexpr int kMost = kStreamSets > kList * kList ? kStreamSets : kList * kList;
+  __shared__ float sm[kFinish / 32];
+  __shared__ double ss[kFinish / 32], st[kFinish / 32];
+  __shared__ uint32_t group[kList];
+  __shared__ int count[2];
+  __shared__ Entry cand[K > 0 ? kMost : 1], first[kList];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int p = blockIdx.x;
+  if (K > 0) {
+    if (t < kList) {
+      group[t] = 0;
+      first[t] = Entry{-INFINITY, -1};
+    }
+    if (t < 2) count[t] = 0;
+  }
+  after_previous();
+  // what the kernel before wrote is read past L1 (__ldcg): this one may have started before it
+  constexpr int kPer = (kStreamSets + kFinish - 1) / kFinish;
+  const int sets = ctas * kSSegs;
+  Entry e[K > 0 ? kPer : 1];
+  auto entry = [&](int set, int j) {
+    const long long at = static_cast<long long>(p) * sets + set;
+    const float2 r = __ldcg(j == 0 ? a.top + at : a.rest + at * (kList - 1) + (j - 1));
+    return r.x > kFloor ? Entry{r.x, __float_as_int(r.y)} : Entry{-INFINITY, -1};
+  };
+  if (K > 0) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int set = t + u * kFinish;
+      e[u] = set < sets ? entry(set, 0) : Entry{-INFINITY, -1};
+    }
+  }
+  Sums s;
+  for (int c = t; c < ctas; c += kFinish) {
+    const float4 q = __ldcg(a.part + static_cast<long long>(p) * ctas + c);
+    s.join(q.x, q.y, q.z);
+  }
+  warp_join(s.M, s.s, s.t);
+  if (lane == 0) {
+    sm[warp] = s.M;
+    ss[warp] = s.s;
+    st[warp] = s.t;
+  }
+  __syncthreads();
+  if (K > 0) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (e[u].id >= 0) atomicMax(&group[(t + u * kFinish) % kList], ordered(e[u].v));
+  }
+  s.M = lane < kFinish / 32 ? sm[lane] : -INFINITY;
+  s.s = lane < kFinish / 32 ? ss[lane] : 0.0;
+  s.t = lane < kFinish / 32 ? st[lane] : 0.0;
+  warp_join(s.M, s.s, s.t);
+  const double ls = log(s.s);
+  if (t == 0) {
+    if (out.lse != nullptr) out.lse[p] = static_cast<float>(s.M + ls);
+    if (out.entropy != nullptr) out.entropy[p] = static_cast<float>(ls - s.t / s.s);
+    if (a.y != nullptr) {
+      const int y = __ldg(a.y + p);
+      const bool ok = y >= 0 && y < a.V;
+      if (!ok) record_status(ctl, kStatusBadTarget);
+      // against M before log S: z_y - lse would round away what large logits leave
+      if (out.logp != nullptr)
+        out.logp[p] = ok ? static_cast<float>((static_cast<double>(__ldcg(a.zy + p)) - s.M) - ls) : 0.f;
+    }
+  }
+  if (K > 0) {
+    __syncthreads();
+    const float bound = from_ordered(
+        __reduce_min_sync(0xffffffffu, lane < kList ? group[lane] : 0xffffffffu));
+    auto push = [&](bool take, const Entry& x, int* n) {      // whole warps call
+      const uint32_t m = __ballot_sync(0xffffffffu, take);
+      if (m == 0) return;
+      int at = 0;
+      if (lane == 0) at = atomicAdd(n, __popc(m));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+      if (take) cand[at] = x;
+    };
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) push(e[u].id >= 0 && e[u].v >= bound, e[u], &count[0]);
+    __syncthreads();
+    auto rank = [&](const Entry& x, int n) {
+      int r = 0;
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) r += ahead(cand[k], x) ? 1 : 0;
+      return r;
+    };
+    const int n1 = count[0];
+    for (int k = t; k < n1; k += kFinish) {
+      const Entry x = cand[k];
+      const int r = rank(x, n1);
+      if (r < kList) first[r] = x;
+    }
+    __syncthreads();
+    // cand from here on: the K first, and the further entries ahead of the last of them: several
+    // per list at a time, until no list's last one looked at is
+    push(t < kList && first[t < kList ? t : 0].id >= 0, first[t < kList ? t : 0], &count[1]);
+    constexpr int kAhead = list_batch(K);
+    const Entry last = first[kList - 1];
+    const Entry f = t < kList * kAhead ? first[t / (kAhead > 0 ? kAhead : 1)] : Entry{0.f, -1};
+    const int set = f.id >= 0 ? StreamSplit{a.V, ctas, a.rows}.list_of(f.id) : 0;
+    bool more = kAhead > 0;
+    for (int j0 = 1; j0 < kList && more; j0 += kAhead) {
+      const int j = j0 + t % (kAhead > 0 ? kAhead : 1);
+      Entry x{-INFINITY, -1};
+      if (f.id >= 0 && j < kList) x = entry(set, j);
+      const bool take = x.id >= 0 && (last.id < 0 || ahead(x, last));
+      push(take, x, &count[1]);
+      more = __syncthreads_or(take && j + 1 - j0 == kAhead) != 0;
+    }
+    __syncthreads();
+    const int n2 = count[1];
+    for (int k = t; k < n2; k += kFinish) {
+      const Entry x = cand[k];
+      const int r = rank(x, n2);
+      if (r < out.n_top) {
+        out.top_ids[static_cast<long long>(p) * out.n_top + r] = x.id;
+        out.top_logp[static_cast<long long>(p) * out.n_top + r] =
+            static_cast<float>((x.v - static_cast<double>(s.M)) - ls);
+      }
+    }
+    for (int r = n2 + t; r < out.n_top; r += kFinish) {       // fewer logits than asked for
+      out.top_ids[static_cast<long long>(p) * out.n_top + r] = -1;
+      out.top_logp[static_cast<long long>(p) * out.n_top + r] = -INFINITY;
+    }
+  }
+}
+
 template <int NT, int K>
 cudaError_t stream_launch(const CUtensorMap& mW, const CUtensorMap& mH, const StreamArgs& a,
                           int grid, const DevCtl& ctl, cudaStream_t st) {
@@ -392,14 +537,22 @@ cudaError_t stream_launch(const CUtensorMap& mW, const CUtensorMap& mH, const St
 }
 
 template <int K>
-cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mH,
-                                const StreamArgs& a, int grid,
-                                const DevCtl& ctl, cudaStream_t st) {
+cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mH, const StreamArgs& a,
+                                int ctas, const StatsOut& out, const DevCtl& ctl,
+                                cudaStream_t st) {
+  cudaError_t e;
   switch (stats_stream_cols(a.n)) {
-    case 16: return stream_launch<16, K>(mW, mH, a, grid, ctl, st);
-    case 32: return stream_launch<32, K>(mW, mH, a, grid, ctl, st);
-    default: return stream_launch<64, K>(mW, mH, a, grid, ctl, st);
+    case 16: e = stream_launch<16, K>(mW, mH, a, ctas, ctl, st); break;
+    case 32: e = stream_launch<32, K>(mW, mH, a, ctas, ctl, st); break;
+    default: e = stream_launch<64, K>(mW, mH, a, ctas, ctl, st); break;
   }
+  if (e != cudaSuccess) return e;
+  // the same split of the SMs' memory as the kernel before: another split would wait for the SMs
+  // to drain and change over (140 us instead of 132 us for 48 positions with 20 alternatives)
+  e = cudaFuncSetAttribute(k_stats_stream_finish<K>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                           cudaSharedmemCarveoutMaxShared);
+  if (e != cudaSuccess) return e;
+  return launch_after(k_stats_stream_finish<K>, dim3(a.n), kFinish, st, a, ctas, out, ctl);
 }
 
 }  // namespace
@@ -417,21 +570,16 @@ int stats_stream_rows(int V, int ctas) {
 }
 
 cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapH,
-                                const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
-                                int ctas, const DevCtl& ctl, cudaStream_t st) {
-  const int K = stats_list_len(n_top);
-  if (K > 0) {
-    const cudaError_t e =
-        cudaMemsetAsync(b.tau, 0, sizeof(uint32_t) * static_cast<size_t>(K) * b.ldp, st);
-    if (e != cudaSuccess) return e;
-  }
-  const StreamArgs a{y, b.part, b.tsum, b.zy, b.tau, b.list, n, V, (d + kBK - 1) / kBK, b.ldp,
-                     stats_stream_rows(V, ctas)};
-  switch (K) {
-    case 0: return stream_by_positions<0>(mapW, mapH, a, ctas, ctl, st);
-    case 1: return stream_by_positions<1>(mapW, mapH, a, ctas, ctl, st);
-    case 8: return stream_by_positions<8>(mapW, mapH, a, ctas, ctl, st);
-    default: return stream_by_positions<32>(mapW, mapH, a, ctas, ctl, st);
+                                const StatsBuf& b, const StatsOut& out, int n, int V, int d,
+                                const int* y, int ctas, const DevCtl& ctl, cudaStream_t st) {
+  const size_t sets = static_cast<size_t>(n) * ctas * kSSegs;
+  const StreamArgs a{y, reinterpret_cast<float4*>(b.part), b.zy, b.list, b.list + sets, n, V,
+                     (d + kBK - 1) / kBK, stats_stream_rows(V, ctas)};
+  switch (stats_list_len(out.n_top)) {
+    case 0: return stream_by_positions<0>(mapW, mapH, a, ctas, out, ctl, st);
+    case 1: return stream_by_positions<1>(mapW, mapH, a, ctas, out, ctl, st);
+    case 8: return stream_by_positions<8>(mapW, mapH, a, ctas, out, ctl, st);
+    default: return stream_by_positions<32>(mapW, mapH, a, ctas, out, ctl, st);
   }
 }
 
