@@ -506,6 +506,7 @@ StatsPlan stats_layout(size_t prefix, long long n_lp, long long n, int V, bool b
     const size_t sets = static_cast<size_t>(n) * stats_stream_ctas(V, kStreamCtas);
     s.off_part = take(sizeof(float4) * sets);
     s.off_zy = take(sizeof(float) * static_cast<size_t>(n));
+    s.off_tau = take(sizeof(uint32_t) * static_cast<size_t>(n) * K);
     s.off_list = take(sizeof(float2) * sets * kStreamLists * K);
   } else {
     const size_t tiles = stats_tiles(bf16, V);

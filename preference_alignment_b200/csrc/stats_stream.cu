@@ -35,7 +35,7 @@ struct StreamShape {
   static constexpr int kPitch = kSRows + 1;                // of z: odd, so columns spread over banks
   static constexpr int kZ = NT * kPitch * 4;               // z[position][row], later the sums
   static constexpr int kSmem =
-      kStages * kStage + kZ + NT * 4 + kSSegs * NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
+      kStages * kStage + kZ + NT * 4 + 2 * kSSegs * NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
   static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -82,6 +82,13 @@ __device__ __forceinline__ bool warps_all(bool mine) {
   return all != 0;
 }
 
+// Long lists: a new logit costs a pass over the list, 12 us for the first tile and 38 us for the
+// eight after it at K = 32 and 48 positions. Bids between the CTAs, as the GEMM route's tiles make
+// them (stats.cu), leave the eight 9 us. Lists of 8 cost 16 us in all without, and the bids' zeroing
+// a launch; they have none.
+constexpr int kBidGroups = 32;
+constexpr bool has_bids(int K) { return K >= kBidGroups; }
+
 constexpr int kFinish = 256;    // threads of the finish: a block per position
 // Further list entries the finish looks at together, one per thread for each of the K lists.
 __host__ __device__ constexpr int list_batch(int K) {
@@ -95,6 +102,7 @@ struct StreamArgs {
   float* zy;            // [n]
   float2* top;          // [n, CTAs * kSSegs] the lists' first entries (logit, id)
   float2* rest;         // [n, CTAs * kSSegs, K - 1] and the others
+  uint32_t* bids;       // [kBidGroups, n] (K = 32), zeroed before the launch
   int n, V, k_blocks;
   int rows;             // vocabulary rows per tile
 };
@@ -116,7 +124,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
   float* z = reinterpret_cast<float*>(sH + kStages * Sh::kHBytes);
   int* sy = reinterpret_cast<int*>(z + NT * Sh::kPitch);
   float* share = reinterpret_cast<float*>(sy + NT);    // [kSSegs][NT]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(share + kSSegs * NT);
+  uint32_t* bound = reinterpret_cast<uint32_t*>(share + kSSegs * NT);   // [kSSegs][NT] of the bids
+  uint64_t* bars = reinterpret_cast<uint64_t*>(bound + kSSegs * NT);
   // bars: [0, S) full, [S, 2S) empty, 2S + {0,1} acc_full, 2S + {2,3} acc_empty, 2S + 4 drain
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -241,6 +250,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
     const bool mine = pt < NT * kSSegs && p < a.n;
     const int set = blockIdx.x * kSSegs + seg;
     float m = kFloor, s = 0.f, tt = 0.f;
+    float bid = kFloor;                     // the largest logit bid so far
     float val[kList];
     int id[kList];
 #pragma unroll
@@ -260,6 +270,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
         break;
       }
       tc_fence_after();
+      uint32_t low_bid = 0xffffffffu;         // this thread's share of the groups
+      if (has_bids(K) && mine) {
+#pragma unroll
+        for (int g = 0; g < kBidGroups / kSSegs; ++g)
+          low_bid = min(low_bid, __ldcg(a.bids + (seg * (kBidGroups / kSSegs) + g) * a.n + p));
+      }
       {
         uint32_t v[kCols];
         tmem_cols<kCols>(tmem_base + lanes + acc * NT + c0, v);
@@ -270,6 +286,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         for (int c = 0; c < kCols; ++c)
           z[(c0 + c) * kPitch + quad * 32 + lane] = __uint_as_float(v[c]);
       }
+      if (has_bids(K) && mine) bound[seg * NT + p] = low_bid;
       warps_sync();
       const int r0 = split.first(blockIdx.x, t);
       const int rows = min(a.rows, a.V - r0);
@@ -307,15 +324,26 @@ __global__ void __launch_bounds__(kSThreads, 1)
           for (int g = 1; g < kSSegs; ++g) all = fminf(all, share[g * NT + p]);
           low = fmaxf(low, all);
         }
-        uint32_t hit = 0;
-        if (mine && cm > low) {
+        float tauv = -INFINITY;
+        if (has_bids(K) && mine) {
+          uint32_t th = bound[p];
 #pragma unroll
-          for (int j = 0; j < kSegRows; ++j) hit |= (x[j] > low ? 1u : 0u) << j;
+          for (int g = 1; g < kSSegs; ++g) th = min(th, bound[g * NT + p]);
+          tauv = from_ordered(th);
+        }
+        uint32_t hit = 0;
+        if (mine && cm > low && cm >= tauv) {
+#pragma unroll
+          for (int j = 0; j < kSegRows; ++j) hit |= (x[j] > low && x[j] >= tauv ? 1u : 0u) << j;
         }
         while (hit != 0) {
           const int j = __ffs(hit) - 1;
           hit &= hit - 1;
           insert_sorted<kList>(val, id, zp[j], r0 + seg * kSegRows + j);
+        }
+        if (has_bids(K) && mine && t + 1 < tiles && val[0] > bid) {
+          bid = val[0];
+          atomicMax(a.bids + set % kBidGroups * a.n + p, ordered(bid));
         }
         // read after the next tile's barrier
         if (K >= kSSegs && mine) share[seg * NT + p] = val[kList >= kSSegs ? kList / kSSegs - 1 : 0];
@@ -382,15 +410,17 @@ __global__ void __launch_bounds__(kSThreads, 1)
   }
 }
 
-// One block per position joins the CTAs' sums and lists.
+// One block per position joins the CTAs' sums and lists. W has just run through L2 and pushed this
+// kernel's instructions out, so its time is the number of instruction lines it fetches from HBM
+// as much as anything: loops are rolled, sums are fp32 (148 terms), and one piece of code joins
+// lanes and warps. (Unrolled and in fp64 it took 7 us at K = 8 and 15 us at K = 32.)
 //
 // Alternatives, all without a chain of insertions: (1) the first entries of the lists, dealt out
 // over K groups, give K different logits, the groups' maxima, so the smallest of those is a lower
 // bound of the K-th largest first entry, which about K log K of them reach; (2) each of these
 // counts how many are ahead of it, its rank: the K first are the lists that can hold any of the K
 // largest logits; (3) the further entries of those lists that are ahead of the K-th so far join
-// them, and their ranks are the answer. (Inserting one by one in a warp took 12 us instead of 5
-// us at K = 8.)
+// them, and their ranks are the answer.
 constexpr int kStreamSets = kStreamCtas * kSSegs;
 
 template <int K>
@@ -398,129 +428,118 @@ __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, i
                                                                  StatsOut out, DevCtl ctl) {
   constexpr int kList = K > 0 ? K : 1;
   constexpr int kMost = kStreamSets > kList * kList ? kStreamSets : kList * kList;
-  __shared__ float sm[kFinish / 32];
-  __shared__ double ss[kFinish / 32], st[kFinish / 32];
+  static_assert(kStreamCtas <= kFinish, "a thread per CTA");
+  __shared__ float4 sums[kFinish / 32];
   __shared__ uint32_t group[kList];
   __shared__ int count[2];
-  __shared__ Entry cand[K > 0 ? kMost : 1], first[kList];
+  __shared__ Entry tops[K > 0 ? kStreamSets : 1], cand[K > 0 ? kMost : 1], first[kList];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int p = blockIdx.x;
+  const int sets = ctas * kSSegs;
   if (K > 0) {
     if (t < kList) {
       group[t] = 0;
       first[t] = Entry{-INFINITY, -1};
     }
     if (t < 2) count[t] = 0;
+    __syncthreads();
   }
   after_previous();
-  // what the kernel before wrote is read past L1 (__ldcg): this one may have started before it
-  constexpr int kPer = (kStreamSets + kFinish - 1) / kFinish;
-  const int sets = ctas * kSSegs;
-  Entry e[K > 0 ? kPer : 1];
-  auto entry = [&](int set, int j) {
-    const long long at = static_cast<long long>(p) * sets + set;
-    const float2 r = __ldcg(j == 0 ? a.top + at : a.rest + at * (kList - 1) + (j - 1));
-    return r.x > kFloor ? Entry{r.x, __float_as_int(r.y)} : Entry{-INFINITY, -1};
-  };
+  float4 q = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  if (t < ctas) q = __ldcg(a.part + static_cast<long long>(p) * ctas + t);
   if (K > 0) {
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int set = t + u * kFinish;
-      e[u] = set < sets ? entry(set, 0) : Entry{-INFINITY, -1};
+#pragma unroll 1
+    for (int k = t; k < sets; k += kFinish) {
+      const float2 r = __ldcg(a.top + static_cast<long long>(p) * sets + k);
+      tops[k] = r.x > kFloor ? Entry{r.x, __float_as_int(r.y)} : Entry{-INFINITY, -1};
+      if (r.x > kFloor) atomicMax(&group[k % kList], ordered(r.x));
     }
   }
-  Sums s;
-  for (int c = t; c < ctas; c += kFinish) {
-    const float4 q = __ldcg(a.part + static_cast<long long>(p) * ctas + c);
-    s.join(q.x, q.y, q.z);
-  }
-  warp_join(s.M, s.s, s.t);
-  if (lane == 0) {
-    sm[warp] = s.M;
-    ss[warp] = s.s;
-    st[warp] = s.t;
-  }
-  __syncthreads();
-  if (K > 0) {
+  // lanes, then warps: the same code twice
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    const float top = from_ordered(__reduce_max_sync(0xffffffffu, ordered(q.x)));
+    if (q.x != top) {                                  // also where both are infinite
+      const float back = q.x - top, f = ex2_approx(back * kLog2eS);
+      q.z = q.x == -INFINITY ? 0.f : f * fmaf(q.y, back, q.z);
+      q.y = q.x == -INFINITY ? 0.f : f * q.y;
+    }
+    q.x = top;
 #pragma unroll
-    for (int u = 0; u < kPer; ++u)
-      if (e[u].id >= 0) atomicMax(&group[(t + u * kFinish) % kList], ordered(e[u].v));
+    for (int o = 16; o > 0; o >>= 1) {
+      q.y += __shfl_xor_sync(0xffffffffu, q.y, o);
+      q.z += __shfl_xor_sync(0xffffffffu, q.z, o);
+    }
+    if (round == 0) {
+      if (lane == 0) sums[warp] = q;
+      __syncthreads();
+      q = lane < kFinish / 32 ? sums[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    }
   }
-  s.M = lane < kFinish / 32 ? sm[lane] : -INFINITY;
-  s.s = lane < kFinish / 32 ? ss[lane] : 0.0;
-  s.t = lane < kFinish / 32 ? st[lane] : 0.0;
-  warp_join(s.M, s.s, s.t);
-  const double ls = log(s.s);
+  const float ls = logf(q.y);
   if (t == 0) {
-    if (out.lse != nullptr) out.lse[p] = static_cast<float>(s.M + ls);
-    if (out.entropy != nullptr) out.entropy[p] = static_cast<float>(ls - s.t / s.s);
+    if (out.lse != nullptr) out.lse[p] = q.x + ls;
+    if (out.entropy != nullptr) out.entropy[p] = ls - __fdividef(q.z, q.y);
     if (a.y != nullptr) {
       const int y = __ldg(a.y + p);
       const bool ok = y >= 0 && y < a.V;
       if (!ok) record_status(ctl, kStatusBadTarget);
       // against M before log S: z_y - lse would round away what large logits leave
-      if (out.logp != nullptr)
-        out.logp[p] = ok ? static_cast<float>((static_cast<double>(__ldcg(a.zy + p)) - s.M) - ls) : 0.f;
+      if (out.logp != nullptr) out.logp[p] = ok ? (__ldcg(a.zy + p) - q.x) - ls : 0.f;
     }
   }
   if (K > 0) {
-    __syncthreads();
     const float bound = from_ordered(
         __reduce_min_sync(0xffffffffu, lane < kList ? group[lane] : 0xffffffffu));
-    auto push = [&](bool take, const Entry& x, int* n) {      // whole warps call
-      const uint32_t m = __ballot_sync(0xffffffffu, take);
-      if (m == 0) return;
-      int at = 0;
-      if (lane == 0) at = atomicAdd(n, __popc(m));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-      if (take) cand[at] = x;
-    };
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) push(e[u].id >= 0 && e[u].v >= bound, e[u], &count[0]);
-    __syncthreads();
-    auto rank = [&](const Entry& x, int n) {
-      int r = 0;
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) r += ahead(cand[k], x) ? 1 : 0;
-      return r;
-    };
-    const int n1 = count[0];
-    for (int k = t; k < n1; k += kFinish) {
-      const Entry x = cand[k];
-      const int r = rank(x, n1);
-      if (r < kList) first[r] = x;
+#pragma unroll 1
+    for (int k = t; k < sets; k += kFinish) {
+      const Entry e = tops[k];
+      if (e.id >= 0 && e.v >= bound) cand[atomicAdd(&count[0], 1)] = e;
     }
-    __syncthreads();
-    // cand from here on: the K first, and the further entries ahead of the last of them: several
-    // per list at a time, until no list's last one looked at is
-    push(t < kList && first[t < kList ? t : 0].id >= 0, first[t < kList ? t : 0], &count[1]);
+    // ranks twice: of the first entries, then of all that can be among the K largest
     constexpr int kAhead = list_batch(K);
-    const Entry last = first[kList - 1];
-    const Entry f = t < kList * kAhead ? first[t / (kAhead > 0 ? kAhead : 1)] : Entry{0.f, -1};
-    const int set = f.id >= 0 ? StreamSplit{a.V, ctas, a.rows}.list_of(f.id) : 0;
-    bool more = kAhead > 0;
-    for (int j0 = 1; j0 < kList && more; j0 += kAhead) {
-      const int j = j0 + t % (kAhead > 0 ? kAhead : 1);
-      Entry x{-INFINITY, -1};
-      if (f.id >= 0 && j < kList) x = entry(set, j);
-      const bool take = x.id >= 0 && (last.id < 0 || ahead(x, last));
-      push(take, x, &count[1]);
-      more = __syncthreads_or(take && j + 1 - j0 == kAhead) != 0;
-    }
-    __syncthreads();
-    const int n2 = count[1];
-    for (int k = t; k < n2; k += kFinish) {
-      const Entry x = cand[k];
-      const int r = rank(x, n2);
-      if (r < out.n_top) {
-        out.top_ids[static_cast<long long>(p) * out.n_top + r] = x.id;
-        out.top_logp[static_cast<long long>(p) * out.n_top + r] =
-            static_cast<float>((x.v - static_cast<double>(s.M)) - ls);
+#pragma unroll 1
+    for (int round = 0; round < 2; ++round) {
+      __syncthreads();
+      const int n = count[round];
+#pragma unroll 1
+      for (int k = t; k < n; k += kFinish) {
+        const Entry x = cand[k];
+        int r = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) r += ahead(cand[j], x) ? 1 : 0;
+        if (r < kList) first[r] = x;
+      }
+      __syncthreads();
+      if (round == 0) {
+        // cand from here on: the K first, and the further entries ahead of the last of them:
+        // several per list at a time, until no list's last one looked at is
+        if (t < kList && first[t].id >= 0) cand[atomicAdd(&count[1], 1)] = first[t];
+        const Entry last = first[kList - 1];
+        const Entry f = t < kList * kAhead ? first[t / (kAhead > 0 ? kAhead : 1)] : Entry{0.f, -1};
+        const int set = f.id >= 0 ? StreamSplit{a.V, ctas, a.rows}.list_of(f.id) : 0;
+        const float2* rest = a.rest + (static_cast<long long>(p) * sets + set) * (kList - 1) - 1;
+        bool more = kAhead > 0;
+#pragma unroll 1
+        for (int j0 = 1; j0 < kList && more; j0 += kAhead) {
+          const int j = j0 + t % (kAhead > 0 ? kAhead : 1);
+          bool take = false;
+          if (f.id >= 0 && j < kList) {
+            const float2 r = __ldcg(rest + j);
+            const Entry x{r.x, __float_as_int(r.y)};
+            take = r.x > kFloor && (last.id < 0 || ahead(x, last));
+            if (take) cand[atomicAdd(&count[1], 1)] = x;
+          }
+          more = __syncthreads_or(take && j + 1 - j0 == kAhead) != 0;
+        }
       }
     }
-    for (int r = n2 + t; r < out.n_top; r += kFinish) {       // fewer logits than asked for
-      out.top_ids[static_cast<long long>(p) * out.n_top + r] = -1;
-      out.top_logp[static_cast<long long>(p) * out.n_top + r] = -INFINITY;
+    // `first` now holds the answer; where there are fewer logits than asked for, the rest is empty
+    if (t < out.n_top) {
+      const Entry x = t < count[1] ? first[t] : Entry{-INFINITY, -1};
+      out.top_ids[static_cast<long long>(p) * out.n_top + t] = x.id;
+      out.top_logp[static_cast<long long>(p) * out.n_top + t] =
+          x.id >= 0 ? (x.v - q.x) - ls : -INFINITY;
     }
   }
 }
@@ -540,7 +559,9 @@ template <int K>
 cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mH, const StreamArgs& a,
                                 int ctas, const StatsOut& out, const DevCtl& ctl,
                                 cudaStream_t st) {
-  cudaError_t e;
+  cudaError_t e = cudaSuccess;
+  if (has_bids(K)) e = cudaMemsetAsync(a.bids, 0, sizeof(uint32_t) * kBidGroups * a.n, st);
+  if (e != cudaSuccess) return e;
   switch (stats_stream_cols(a.n)) {
     case 16: e = stream_launch<16, K>(mW, mH, a, ctas, ctl, st); break;
     case 32: e = stream_launch<32, K>(mW, mH, a, ctas, ctl, st); break;
@@ -573,7 +594,7 @@ cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapH
                                 const StatsBuf& b, const StatsOut& out, int n, int V, int d,
                                 const int* y, int ctas, const DevCtl& ctl, cudaStream_t st) {
   const size_t sets = static_cast<size_t>(n) * ctas * kSSegs;
-  const StreamArgs a{y, reinterpret_cast<float4*>(b.part), b.zy, b.list, b.list + sets, n, V,
+  const StreamArgs a{y, reinterpret_cast<float4*>(b.part), b.zy, b.list, b.list + sets, b.tau, n, V,
                      (d + kBK - 1) / kBK, stats_stream_rows(V, ctas)};
   switch (stats_list_len(out.n_top)) {
     case 0: return stream_by_positions<0>(mapW, mapH, a, ctas, out, ctl, st);
