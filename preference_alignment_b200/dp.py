@@ -15,6 +15,9 @@ all chosen completion tokens of all ranks), so:
    dH, which needs no exchange, while the last block's all-reduce runs;
 4. `allreduce_shares` sums the loss shares (one small all-reduce).
 
+With a `FinalNorm` the exchange goes on through the norm before the head: dx from dH, and its
+weight gradients summed over the ranks with dW's blocks.
+
 dH stays on its rank. This mirrors the data-parallel replicas of the pages'
 systems ("Run Distributed Full-Model DPO with PyTorch FSDP", Step 1: every rank
 holds part of the global batch and the gradients are summed; Megatron-Bridge PR
@@ -73,22 +76,51 @@ def allreduce_shares(shares, group=None):
     return shares
 
 
+class FinalNorm:
+    """The model's final norm (the head's H is its output) as the backward exchange takes it: what
+    its forward kept and where its gradients go. x is the forward's input [rows, d], or the
+    libdpo.Checkpoint that holds it in 8 bits; mean (None for "rms") and rstd are the forward's
+    statistics; dx, dweight and dbias are written (any of them may be None); ws is norm_backward's
+    workspace. dx stays on its rank, dweight and dbias are summed over the ranks."""
+
+    def __init__(self, x, mean, rstd, dx, weight=None, dweight=None, dbias=None, kind="layer",
+                 ws=None):
+        self.x, self.mean, self.rstd, self.dx, self.weight = x, mean, rstd, dx, weight
+        self.dweight, self.dbias, self.kind, self.ws = dweight, dbias, kind, ws
+
+    def backward(self, dH, ops):
+        """The norm's gradients at dH [R, L, d], on the current stream."""
+        ops.norm_backward(self.x, dH, self.mean, self.rstd, dx=self.dx, weight=self.weight,
+                          dweight=self.dweight, dbias=self.dbias, kind=self.kind, ws=self.ws)
+
+    def reduced(self):
+        return [g for g in (self.dweight, self.dbias) if g is not None]
+
+
 def backward_exchange(batch, lse_state, row_coef, dH, dW, ws, n_buckets=8, max_sms=0,
-                      group=None):
+                      group=None, norm=None, ops=None):
     """The data-parallel backward on this rank: dz once (dpo_backward with dW = NULL),
     then dW block by block with each block's all-reduce started as soon as it is
-    formed, then dH while the last all-reduce runs. max_sms > 0 leaves the other SMs
-    free for the collective's kernels. Everything is enqueued on torch's current
-    stream, the stream the collectives order against. Returns the pending works
-    (finish() them)."""
-    from preference_alignment_b200 import libdpo
-    libdpo.backward(batch, lse_state, row_coef, None, None, False, ws)
+    formed, then dH while the last all-reduce runs, then (norm: a FinalNorm) the final
+    norm's backward on that dH, whose weight gradients are all-reduced as well. max_sms > 0
+    leaves the other SMs free for the collective's kernels. Everything is enqueued on
+    torch's current stream, the stream the collectives order against. Returns the pending
+    works (finish() them). ops: the calls to make (default: the library)."""
+    import torch.distributed as dist
+    if ops is None:
+        from preference_alignment_b200 import libdpo as ops
+    if norm is not None and dH is None:
+        raise ValueError("the final norm's backward needs dH")
+    ops.backward(batch, lse_state, row_coef, None, None, False, ws)
     works = bucketed_allreduce(
         dW, vocab_buckets(int(batch.c.V), n_buckets),
-        lambda v0, v1: libdpo.backward_dw(batch, v0, v1, dW, False, ws, max_sms=max_sms),
+        lambda v0, v1: ops.backward_dw(batch, v0, v1, dW, False, ws, max_sms=max_sms),
         group=group)
     if dH is not None:
-        libdpo.backward_dh(batch, dH, ws, max_sms=max_sms)
+        ops.backward_dh(batch, dH, ws, max_sms=max_sms)
+    if norm is not None:
+        norm.backward(dH, ops)
+        works += [dist.all_reduce(g, group=group, async_op=True) for g in norm.reduced()]
     return works
 
 
