@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
         if (has_bids(K) && mine && t + 1 < tiles && val[0] > bid) {
           bid = val[0];
-          atomicMax(a.bids + set % kBidGroups * a.n + p, ordered(bid));
+          atomicMax(a.bids + blockIdx.x % kBidGroups * a.n + p, ordered(bid));
         }
         // read after the next tile's barrier
         if (K >= kSSegs && mine) share[seg * NT + p] = val[kList >= kSSegs ? kList / kSSegs - 1 : 0];
@@ -423,6 +423,17 @@ __global__ void __launch_bounds__(kSThreads, 1)
 // them, and their ranks are the answer.
 constexpr int kStreamSets = kStreamCtas * kSSegs;
 
+// A list entry (logit, id) as one number: greater is ahead (the larger logit, then the lower id);
+// 0 stands for none.
+__device__ __forceinline__ unsigned long long entry_key(const float2& r) {
+  return r.x > kFloor ? static_cast<unsigned long long>(ordered(r.x)) << 32 |
+                            static_cast<uint32_t>(~__float_as_int(r.y))
+                      : 0ull;
+}
+__device__ __forceinline__ int key_id(unsigned long long k) {
+  return ~static_cast<int>(static_cast<uint32_t>(k));
+}
+
 template <int K>
 __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, int ctas,
                                                                  StatsOut out, DevCtl ctl) {
@@ -432,14 +443,14 @@ __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, i
   __shared__ float4 sums[kFinish / 32];
   __shared__ uint32_t group[kList];
   __shared__ int count[2];
-  __shared__ Entry tops[K > 0 ? kStreamSets : 1], cand[K > 0 ? kMost : 1], first[kList];
+  __shared__ unsigned long long tops[K > 0 ? kStreamSets : 1], cand[K > 0 ? kMost : 1], first[kList];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int p = blockIdx.x;
   const int sets = ctas * kSSegs;
   if (K > 0) {
     if (t < kList) {
       group[t] = 0;
-      first[t] = Entry{-INFINITY, -1};
+      first[t] = 0;
     }
     if (t < 2) count[t] = 0;
     __syncthreads();
@@ -451,8 +462,9 @@ __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, i
 #pragma unroll 1
     for (int k = t; k < sets; k += kFinish) {
       const float2 r = __ldcg(a.top + static_cast<long long>(p) * sets + k);
-      tops[k] = r.x > kFloor ? Entry{r.x, __float_as_int(r.y)} : Entry{-INFINITY, -1};
-      if (r.x > kFloor) atomicMax(&group[k % kList], ordered(r.x));
+      tops[k] = entry_key(r);
+      // by CTA: a short tile leaves some segments without rows, and a group without logits bounds nothing
+      if (r.x > kFloor) atomicMax(&group[k / kSSegs % kList], ordered(r.x));
     }
   }
   // lanes, then warps: the same code twice
@@ -489,12 +501,13 @@ __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, i
     }
   }
   if (K > 0) {
-    const float bound = from_ordered(
-        __reduce_min_sync(0xffffffffu, lane < kList ? group[lane] : 0xffffffffu));
+    const unsigned long long bound =
+        static_cast<unsigned long long>(
+            __reduce_min_sync(0xffffffffu, lane < kList ? group[lane] : 0xffffffffu)) << 32;
 #pragma unroll 1
     for (int k = t; k < sets; k += kFinish) {
-      const Entry e = tops[k];
-      if (e.id >= 0 && e.v >= bound) cand[atomicAdd(&count[0], 1)] = e;
+      const unsigned long long e = tops[k];
+      if (e != 0 && e >= bound) cand[atomicAdd(&count[0], 1)] = e;
     }
     // ranks twice: of the first entries, then of all that can be among the K largest
     constexpr int kAhead = list_batch(K);
@@ -504,30 +517,29 @@ __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, i
       const int n = count[round];
 #pragma unroll 1
       for (int k = t; k < n; k += kFinish) {
-        const Entry x = cand[k];
+        const unsigned long long x = cand[k];
         int r = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) r += ahead(cand[j], x) ? 1 : 0;
+        for (int j = 0; j < n; ++j) r += cand[j] > x ? 1 : 0;
         if (r < kList) first[r] = x;
       }
       __syncthreads();
       if (round == 0) {
         // cand from here on: the K first, and the further entries ahead of the last of them:
         // several per list at a time, until no list's last one looked at is
-        if (t < kList && first[t].id >= 0) cand[atomicAdd(&count[1], 1)] = first[t];
-        const Entry last = first[kList - 1];
-        const Entry f = t < kList * kAhead ? first[t / (kAhead > 0 ? kAhead : 1)] : Entry{0.f, -1};
-        const int set = f.id >= 0 ? StreamSplit{a.V, ctas, a.rows}.list_of(f.id) : 0;
+        if (t < kList && first[t] != 0) cand[atomicAdd(&count[1], 1)] = first[t];
+        const unsigned long long last = first[kList - 1];
+        const unsigned long long f = t < kList * kAhead ? first[t / (kAhead > 0 ? kAhead : 1)] : 0;
+        const int set = f != 0 ? StreamSplit{a.V, ctas, a.rows}.list_of(key_id(f)) : 0;
         const float2* rest = a.rest + (static_cast<long long>(p) * sets + set) * (kList - 1) - 1;
         bool more = kAhead > 0;
 #pragma unroll 1
         for (int j0 = 1; j0 < kList && more; j0 += kAhead) {
           const int j = j0 + t % (kAhead > 0 ? kAhead : 1);
           bool take = false;
-          if (f.id >= 0 && j < kList) {
-            const float2 r = __ldcg(rest + j);
-            const Entry x{r.x, __float_as_int(r.y)};
-            take = r.x > kFloor && (last.id < 0 || ahead(x, last));
+          if (f != 0 && j < kList) {
+            const unsigned long long x = entry_key(__ldcg(rest + j));
+            take = x > last;
             if (take) cand[atomicAdd(&count[1], 1)] = x;
           }
           more = __syncthreads_or(take && j + 1 - j0 == kAhead) != 0;
@@ -536,10 +548,10 @@ __global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, i
     }
     // `first` now holds the answer; where there are fewer logits than asked for, the rest is empty
     if (t < out.n_top) {
-      const Entry x = t < count[1] ? first[t] : Entry{-INFINITY, -1};
-      out.top_ids[static_cast<long long>(p) * out.n_top + t] = x.id;
+      const unsigned long long x = t < count[1] ? first[t] : 0;
+      out.top_ids[static_cast<long long>(p) * out.n_top + t] = x != 0 ? key_id(x) : -1;
       out.top_logp[static_cast<long long>(p) * out.n_top + t] =
-          x.id >= 0 ? (x.v - q.x) - ls : -INFINITY;
+          x != 0 ? (from_ordered(static_cast<uint32_t>(x >> 32)) - q.x) - ls : -INFINITY;
     }
   }
 }
