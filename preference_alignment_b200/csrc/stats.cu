@@ -296,10 +296,15 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
 }
 
 // ------------------------------------------------------------------ fp32 route
-// Each warp takes 32 vocabulary rows (one tile of partials) for kPos positions: W rows are
-// read once per kPos positions, lanes stride over d, and after the 32 dot products lane l
-// holds z of row l.
-constexpr int kPos = 4;
+// A block takes 32 vocabulary rows (one tile of partials) and 32 positions, a warp 4 of them, a
+// lane one vocabulary row: z = h . w is summed in the lane, over d in pieces that both operands
+// pass through shared memory, and no exchange between lanes is needed before the statistics. W is
+// read once per 32 positions. (With lanes along d, a warp per vocabulary row and five exchanges
+// per logit it took 37 us at 65 positions, V = 1000, d = 64.)
+constexpr int kPos = 4;                  // positions per warp
+constexpr int kF32Rows = 32;             // vocabulary rows per tile
+constexpr int kF32Pos = 8 * kPos;        // positions per block
+constexpr int kF32K = 32;                // values of d per piece
 
 template <int K>
 __global__ void __launch_bounds__(256) k_stats_f32(const float* __restrict__ H,
@@ -310,43 +315,50 @@ __global__ void __launch_bounds__(256) k_stats_f32(const float* __restrict__ H,
                                                    float* __restrict__ tsum,
                                                    float* __restrict__ zy,
                                                    float2* __restrict__ list) {
-  const int lane = threadIdx.x & 31;
-  const int nt = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int v0 = nt * 32;
-  if (v0 >= V) return;
-  const int i0 = blockIdx.y * kPos;
-  const float* h[kPos];
-#pragma unroll
-  for (int q = 0; q < kPos; ++q) {
-    const int i = min(i0 + q, n - 1);
-    h[q] = H + (at != nullptr ? at[i] : i) * h_stride;
+  // rows of 9 groups of 4 values: lanes 8 rows apart start 8 banks apart
+  __shared__ float4 sw[kF32Rows][kF32K / 4 + 1], sh[kF32Pos][kF32K / 4 + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nt = blockIdx.x, v0 = nt * kF32Rows;
+  const int base = blockIdx.y * kF32Pos, i0 = base + warp * kPos;
+  // this thread copies 4 values of one row of each operand per piece
+  const int cr = threadIdx.x >> 3, ck = threadIdx.x & 7;
+  const float* w = W + static_cast<long long>(min(v0 + cr, V - 1)) * d;
+  const int hi = min(base + cr, n - 1);
+  const float* h = H + (at != nullptr ? at[hi] : hi) * h_stride;
+  float z[kPos] = {};
+  const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 cw = none, ch = none;
+  if (ck * 4 < d) {                        // d is a multiple of 8: 4 values are all in or all out
+    cw = __ldg(reinterpret_cast<const float4*>(w) + ck);
+    ch = __ldg(reinterpret_cast<const float4*>(h) + ck);
   }
-  float z[kPos];
+  for (int k0 = 0; k0 < d; k0 += kF32K) {
+    __syncthreads();
+    sw[cr][ck] = cw;
+    sh[cr][ck] = ch;
+    __syncthreads();
+    const int k = k0 + kF32K + ck * 4;     // the next piece while this one is worked on
+    cw = k < d ? __ldg(reinterpret_cast<const float4*>(w + k)) : none;
+    ch = k < d ? __ldg(reinterpret_cast<const float4*>(h + k)) : none;
 #pragma unroll
-  for (int q = 0; q < kPos; ++q) z[q] = -INFINITY;
-  for (int r = 0; r < 32 && v0 + r < V; ++r) {
-    const float* w = W + static_cast<long long>(v0 + r) * d;
-    float a[kPos] = {};
-    for (int k = lane; k < d; k += 32) {
-      const float wk = __ldg(w + k);
+    for (int c = 0; c < kF32K / 4; ++c) {
+      const float4 a = sw[lane][c];
 #pragma unroll
-      for (int q = 0; q < kPos; ++q) a[q] = fmaf(__ldg(h[q] + k), wk, a[q]);
-    }
-#pragma unroll
-    for (int q = 0; q < kPos; ++q) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a[q] += __shfl_xor_sync(0xffffffffu, a[q], o);
-      if (lane == r) z[q] = a[q];
+      for (int q = 0; q < kPos; ++q) {
+        const float4 b = sh[warp * kPos + q][c];
+        z[q] = fmaf(a.x, b.x, z[q]);
+        z[q] = fmaf(a.y, b.y, z[q]);
+        z[q] = fmaf(a.z, b.z, z[q]);
+        z[q] = fmaf(a.w, b.w, z[q]);
+      }
     }
   }
 #pragma unroll
   for (int q = 0; q < kPos; ++q) {
     const int i = i0 + q;
     if (i >= n) break;
-    const float x = z[q];
-    float m = fmaxf(x, kFloor);                 // padding rows hold -inf; a NaN gives the floor
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float x = v0 + lane < V ? z[q] : -INFINITY;
+    const float m = from_ordered(__reduce_max_sync(0xffffffffu, ordered(fmaxf(x, kFloor))));
     const float e = expf(x - m);
     float s = e, t = e > 0.f ? e * (x - m) : (e == 0.f ? 0.f : e);
 #pragma unroll
@@ -361,18 +373,16 @@ __global__ void __launch_bounds__(256) k_stats_f32(const float* __restrict__ H,
     }
     if (y != nullptr && __ldg(y + i) == v0 + lane && v0 + lane < V) zy[i] = x;
     if (K > 0) {
-      Entry best{-INFINITY, -1};
-      for (int r = 0; r < 32; ++r) {            // insertion across the lanes, in rising id
-        const float xr = __shfl_sync(0xffffffffu, x, r);
-        const bool take = xr > kFloor;          // false for NaN
-        const int at_lane = __popc(__ballot_sync(0xffffffffu, best.v >= xr));
-        const Entry up{__shfl_up_sync(0xffffffffu, best.v, 1),
-                       __shfl_up_sync(0xffffffffu, best.id, 1)};
-        if (take) best = lane < at_lane ? best : (lane == at_lane ? Entry{xr, v0 + r} : up);
+      // the lane's rank is the number of rows ahead of it
+      const uint32_t mine = x > kFloor ? ordered(x) : 0u;      // 0: none (NaN included)
+      int rank = 0;
+      for (int r = 0; r < 32; ++r) {
+        const uint32_t other = __shfl_sync(0xffffffffu, mine, r);
+        rank += other > mine || (other == mine && r < lane) ? 1 : 0;
       }
-      if (lane < K)
-        list[(static_cast<long long>(nt) * K + lane) * ldp + i] =
-            make_float2(best.v, __int_as_float(best.id));
+      if (rank < K)
+        list[(static_cast<long long>(nt) * K + rank) * ldp + i] =
+            mine != 0 ? make_float2(x, __int_as_float(v0 + lane)) : make_float2(kFloor, 0.f);
     }
   }
 }
@@ -380,7 +390,10 @@ __global__ void __launch_bounds__(256) k_stats_f32(const float* __restrict__ H,
 // ------------------------------------------------------------------ launches
 int stats_list_len(int n_top) { return n_top == 0 ? 0 : n_top == 1 ? 1 : n_top <= 8 ? 8 : 32; }
 
-int stats_tiles(bool bf16, int V) { return (V + (bf16 ? kBN : 32) - 1) / (bf16 ? kBN : 32); }
+int stats_tiles(bool bf16, int V) {
+  const int rows = bf16 ? kBN : kF32Rows;
+  return (V + rows - 1) / rows;
+}
 
 namespace {
 
@@ -432,7 +445,7 @@ cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, 
                              const StatsBuf& b, int n_top, int n, int V, int d, const int* y,
                              cudaStream_t st) {
   const int K = stats_list_len(n_top);
-  const dim3 grid((stats_tiles(false, V) + 7) / 8, (n + kPos - 1) / kPos);
+  const dim3 grid(stats_tiles(false, V), (n + kF32Pos - 1) / kF32Pos);
   auto kern = K == 0   ? k_stats_f32<0>
               : K == 1 ? k_stats_f32<1>
               : K == 8 ? k_stats_f32<8>
