@@ -12,9 +12,9 @@
 #include <cmath>
 
 #include "internal.h"
-#include "chain.cuh"
 #include "gemm_launch.cuh"
 #include "stats.cuh"
+#include "stats_join.cuh"
 
 namespace dpo {
 
@@ -164,8 +164,44 @@ struct EpiStats {
 };
 
 // ------------------------------------------------------------------ finish
-// WPP warps per position (the block's 8 warps hold 8 / WPP positions): lane l of warp w joins
-// tiles 32 w + l, 32 w + l + 32 WPP, ..., then lanes and warps join in a fixed order.
+// Tiles in id order: the GEMM's or the SIMT route's partials, as the join reads them.
+template <int K>
+struct TileSets {
+  const float2* part;
+  const float* tsum;
+  const float2* list;
+  const uint32_t* tau;       // or nullptr
+  int S, ldp;
+  static constexpr int kFrom = 0;
+  __device__ __forceinline__ int sums() const { return S; }
+  __device__ __forceinline__ float4 sum(int p, int k) const {
+    const long long at = static_cast<long long>(k) * ldp + p;
+    const float2 q = __ldcg(part + at);
+    return make_float4(q.x, q.y, __ldcg(tsum + at), 0.f);
+  }
+  __device__ __forceinline__ int sets() const { return S; }
+  __device__ __forceinline__ uint32_t floor_of(int p, int lane) const {
+    if (tau == nullptr) return 0;
+    return __reduce_min_sync(
+        0xffffffffu, lane < K ? __ldcg(tau + static_cast<long long>(lane) * ldp + p) : 0xffffffffu);
+  }
+  __device__ __forceinline__ unsigned long long key(int p, int k, uint32_t floor) const {
+    const float m = __ldcg(part + static_cast<long long>(k) * ldp + p).x;
+    return ordered(m) >= floor ? entry_key(make_float2(m, __int_as_float(k))) : 0;
+  }
+  template <int KK>
+  __device__ __forceinline__ int group(int k) const {
+    return k % KK;
+  }
+  template <int KK>
+  __device__ __forceinline__ float2 entry(int p, unsigned long long key, int j) const {
+    return __ldcg(list + (static_cast<long long>(key_id(key)) * KK + j) * ldp + p);
+  }
+};
+
+// The join of many positions, or of more tiles than stats_join.cuh's has room for: one warp per
+// position. Lane l joins tiles l, l + 32, ..., then the lanes join in a fixed order (S and T in
+// fp64, so that a vocabulary of millions loses nothing).
 //
 // Alternatives. The K largest logits lie in the K first tiles by (maximum falling, id rising): a
 // logit of any other tile has the maxima of those K ahead of it. So the warp keeps the K first
@@ -173,7 +209,7 @@ struct EpiStats {
 // the tiles' second, third, ... entries go in until none is ahead of the list's last. (Joining
 // every tile's list instead, in one chain of dependent loads, took 230 us of the 435 us of a
 // single token at V = 128,256.)
-template <int K, int WPP>
+template <int K>
 __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__ part,
                                                       const float* __restrict__ tsum,
                                                       const float2* __restrict__ list,
@@ -181,15 +217,9 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
                                                       const float* __restrict__ zy,
                                                       const int* __restrict__ y, int n, int S,
                                                       int V, int ldp, StatsOut out, DevCtl ctl) {
-  constexpr int kJoin = WPP > 1 ? WPP : 1;
-  __shared__ float sm[kJoin];
-  __shared__ double ss[kJoin], st[kJoin];
-  __shared__ float bv[kJoin][32];
-  __shared__ int bi[kJoin][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i = WPP > 1 ? blockIdx.x : blockIdx.x * 8 + warp;
-  const int w = WPP > 1 ? warp : 0;
-  if (i >= n) return;                     // whole warps; whole blocks when WPP > 1
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= n) return;
   after_previous();
   // what the kernel before wrote is read past L1 (__ldcg): this one may have started before it
   constexpr int U = 4;
@@ -199,12 +229,12 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
   Sums a;
   Entry best{-INFINITY, -1};              // tiles by their maximum
   float tauv = 0.f;
-  for (int base = 0; base < S; base += 32 * WPP * U) {
+  for (int base = 0; base < S; base += 32 * U) {
     float2 q[U];
     float tq[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int k = base + (u * WPP + w) * 32 + lane;
+      const int k = base + u * 32 + lane;
       q[u] = make_float2(-INFINITY, 0.f);
       tq[u] = 0.f;
       if (k < S) {
@@ -223,7 +253,7 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
         while (hit) {
           const int src = __ffs(hit) - 1;
           insert_entry(best, Entry{__shfl_sync(0xffffffffu, m, src),
-                                   base + (u * WPP + w) * 32 + src}, lane);
+                                   base + u * 32 + src}, lane);
           hit &= hit - 1;
           hit &= __ballot_sync(0xffffffffu, m > __shfl_sync(0xffffffffu, best.v, K - 1));
         }
@@ -231,31 +261,6 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
     }
   }
   warp_join(a.M, a.s, a.t);
-  if (WPP > 1) {
-    if (lane == 0) {
-      sm[w] = a.M;
-      ss[w] = a.s;
-      st[w] = a.t;
-    }
-    if (K > 0) {
-      // the warps' lists join in pairs
-      for (int r = 1; r < WPP; r *= 2) {
-        if (w % (2 * r) == r) {
-          bv[w][lane] = best.v;
-          bi[w][lane] = best.id;
-        }
-        __syncthreads();
-        if (w % (2 * r) == 0) merge_lists(best, Entry{bv[w + r][lane], bi[w + r][lane]}, lane);
-      }
-    } else {
-      __syncthreads();
-    }
-    if (warp != 0) return;
-    a.M = lane < WPP ? sm[lane] : -INFINITY;
-    a.s = lane < WPP ? ss[lane] : 0.0;
-    a.t = lane < WPP ? st[lane] : 0.0;
-    warp_join(a.M, a.s, a.t);
-  }
   const double ls = log(a.s);
   if (lane == 0) {
     if (out.lse != nullptr) out.lse[i] = static_cast<float>(a.M + ls);
@@ -397,8 +402,8 @@ int stats_tiles(bool bf16, int V) {
 
 namespace {
 
-// Up to this many positions a whole block joins each one's tiles.
-constexpr int kWideFinish = 1024;
+// Up to this many positions a block joins each one's tiles, above it a warp.
+constexpr int kBlockJoin = 1024;
 
 template <int K>
 cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const StatsBuf& b, int n,
@@ -419,11 +424,11 @@ cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, 
                         
                          const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
   const uint32_t* tau = with_tau ? b.tau : nullptr;
-  if (n <= kWideFinish)
-    return launch_after(k_stats_finish<K, 8>, dim3(n), 256, st, b.part, b.tsum, b.list, tau, b.zy, y,
-                        n, S, V, b.ldp, out, ctl);
-  return launch_after(k_stats_finish<K, 1>, dim3((n + 7) / 8), 256, st, b.part, b.tsum, b.list, tau,
-                      b.zy, y, n, S, V, b.ldp, out, ctl);
+  if (n <= kBlockJoin && S <= kJoinSets)
+    return launch_join<K>(TileSets<K>{b.part, b.tsum, b.list, tau, S, b.ldp}, y, b.zy, n, V, out, ctl,
+                          st);
+  return launch_after(k_stats_finish<K>, dim3((n + 7) / 8), 256, st, b.part, b.tsum, b.list, tau, b.zy,
+                      y, n, S, V, b.ldp, out, ctl);
 }
 
 }  // namespace

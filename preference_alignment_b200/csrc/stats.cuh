@@ -35,19 +35,6 @@ __device__ __forceinline__ bool ahead(const Entry& a, const Entry& b) {
   return a.v > b.v || (a.v == b.v && a.id < b.id);
 }
 
-// The 32 best of two falling lists: entry j against entry 31 - j of the other leaves the best
-// 32 in an order that falls and then rises (or the reverse), which five exchange rounds sort.
-__device__ __forceinline__ void merge_lists(Entry& a, Entry b, int lane) {
-  b.v = __shfl_sync(0xffffffffu, b.v, 31 - lane);
-  b.id = __shfl_sync(0xffffffffu, b.id, 31 - lane);
-  if (ahead(b, a)) a = b;
-#pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
-    const Entry o{__shfl_xor_sync(0xffffffffu, a.v, w), __shfl_xor_sync(0xffffffffu, a.id, w)};
-    if (((lane & w) == 0) == ahead(o, a)) a = o;
-  }
-}
-
 // Puts x into a falling list (entry j in lane j), behind every entry ahead of it.
 __device__ __forceinline__ void insert_entry(Entry& list, const Entry& x, int lane) {
   const int at = __popc(__ballot_sync(0xffffffffu, ahead(list, x)));

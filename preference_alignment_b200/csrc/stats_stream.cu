@@ -16,9 +16,9 @@
 // its K largest logits in registers.
 #include <algorithm>
 
-#include "chain.cuh"
 #include "internal.h"
 #include "stats.cuh"
+#include "stats_join.cuh"
 
 namespace dpo {
 
@@ -89,12 +89,6 @@ __device__ __forceinline__ bool warps_all(bool mine) {
 constexpr int kBidGroups = 32;
 constexpr bool has_bids(int K) { return K >= kBidGroups; }
 
-constexpr int kFinish = 256;    // threads of the finish: a block per position
-// Further list entries the finish looks at together, one per thread for each of the K lists.
-__host__ __device__ constexpr int list_batch(int K) {
-  return K <= 1 ? 0 : K * (K - 1) <= kFinish ? K - 1 : kFinish / K;
-}
-
 struct StreamArgs {
   const int* y;         // given tokens, or nullptr
   // by position, so that the finish reads whole lines
@@ -107,6 +101,35 @@ struct StreamArgs {
   int rows;             // vocabulary rows per tile
 };
 
+// Where the join finds this form's results (stats_join.cuh).
+struct StreamSets {
+  const float4* part;
+  const float2 *top, *rest;
+  int V, ctas, rows;
+  static constexpr int kFrom = 1;            // list entries that the sets' keys already are
+  __device__ __forceinline__ int sums() const { return ctas; }
+  __device__ __forceinline__ float4 sum(int p, int k) const {
+    return __ldcg(part + static_cast<long long>(p) * ctas + k);
+  }
+  __device__ __forceinline__ int sets() const { return ctas * kSSegs; }
+  __device__ __forceinline__ uint32_t floor_of(int, int) const { return 0; }
+  __device__ __forceinline__ unsigned long long key(int p, int k, uint32_t) const {
+    return entry_key(__ldcg(top + static_cast<long long>(p) * sets() + k));
+  }
+  // by CTA: a short tile leaves some segments without rows, and a group without logits bounds
+  // nothing
+  template <int K>
+  __device__ __forceinline__ int group(int k) const {
+    return k / kSSegs % K;
+  }
+  template <int K>
+  __device__ __forceinline__ float2 entry(int p, unsigned long long key, int j) const {
+    const int set = StreamSplit{V, ctas, rows}.list_of(key_id(key));
+    return __ldcg(rest + (static_cast<long long>(p) * sets() + set) * (K - 1) + (j - 1));
+  }
+};
+static_assert(kStreamCtas * kSSegs <= kJoinSets, "room for every list");
+
 template <int NT, int K>
 __global__ void __launch_bounds__(kSThreads, 1)
     k_stats_stream(const __grid_constant__ CUtensorMap tmW,
@@ -114,7 +137,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   using Sh = StreamShape<NT>;
   constexpr int kStages = Sh::kStages;
   constexpr int kList = K > 0 ? K : 1;
-  constexpr int kBatch = list_batch(K);
+  constexpr int kBatch = join_batch<K, StreamSets>();
   constexpr int kPitch = Sh::kPitch;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -410,152 +433,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
   }
 }
 
-// One block per position joins the CTAs' sums and lists. W has just run through L2 and pushed this
-// kernel's instructions out, so its time is the number of instruction lines it fetches from HBM
-// as much as anything: loops are rolled, sums are fp32 (148 terms), and one piece of code joins
-// lanes and warps. (Unrolled and in fp64 it took 7 us at K = 8 and 15 us at K = 32.)
-//
-// Alternatives, all without a chain of insertions: (1) the first entries of the lists, dealt out
-// over K groups, give K different logits, the groups' maxima, so the smallest of those is a lower
-// bound of the K-th largest first entry, which about K log K of them reach; (2) each of these
-// counts how many are ahead of it, its rank: the K first are the lists that can hold any of the K
-// largest logits; (3) the further entries of those lists that are ahead of the K-th so far join
-// them, and their ranks are the answer.
-constexpr int kStreamSets = kStreamCtas * kSSegs;
-
-// A list entry (logit, id) as one number: greater is ahead (the larger logit, then the lower id);
-// 0 stands for none.
-__device__ __forceinline__ unsigned long long entry_key(const float2& r) {
-  return r.x > kFloor ? static_cast<unsigned long long>(ordered(r.x)) << 32 |
-                            static_cast<uint32_t>(~__float_as_int(r.y))
-                      : 0ull;
-}
-__device__ __forceinline__ int key_id(unsigned long long k) {
-  return ~static_cast<int>(static_cast<uint32_t>(k));
-}
-
-template <int K>
-__global__ void __launch_bounds__(kFinish) k_stats_stream_finish(StreamArgs a, int ctas,
-                                                                 StatsOut out, DevCtl ctl) {
-  constexpr int kList = K > 0 ? K : 1;
-  constexpr int kMost = kStreamSets > kList * kList ? kStreamSets : kList * kList;
-  static_assert(kStreamCtas <= kFinish, "a thread per CTA");
-  __shared__ float4 sums[kFinish / 32];
-  __shared__ uint32_t group[kList];
-  __shared__ int count[2];
-  __shared__ unsigned long long tops[K > 0 ? kStreamSets : 1], cand[K > 0 ? kMost : 1], first[kList];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int p = blockIdx.x;
-  const int sets = ctas * kSSegs;
-  if (K > 0) {
-    if (t < kList) {
-      group[t] = 0;
-      first[t] = 0;
-    }
-    if (t < 2) count[t] = 0;
-    __syncthreads();
-  }
-  after_previous();
-  float4 q = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-  if (t < ctas) q = __ldcg(a.part + static_cast<long long>(p) * ctas + t);
-  if (K > 0) {
-#pragma unroll 1
-    for (int k = t; k < sets; k += kFinish) {
-      const float2 r = __ldcg(a.top + static_cast<long long>(p) * sets + k);
-      tops[k] = entry_key(r);
-      // by CTA: a short tile leaves some segments without rows, and a group without logits bounds nothing
-      if (r.x > kFloor) atomicMax(&group[k / kSSegs % kList], ordered(r.x));
-    }
-  }
-  // lanes, then warps: the same code twice
-#pragma unroll 1
-  for (int round = 0; round < 2; ++round) {
-    const float top = from_ordered(__reduce_max_sync(0xffffffffu, ordered(q.x)));
-    if (q.x != top) {                                  // also where both are infinite
-      const float back = q.x - top, f = ex2_approx(back * kLog2eS);
-      q.z = q.x == -INFINITY ? 0.f : f * fmaf(q.y, back, q.z);
-      q.y = q.x == -INFINITY ? 0.f : f * q.y;
-    }
-    q.x = top;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      q.y += __shfl_xor_sync(0xffffffffu, q.y, o);
-      q.z += __shfl_xor_sync(0xffffffffu, q.z, o);
-    }
-    if (round == 0) {
-      if (lane == 0) sums[warp] = q;
-      __syncthreads();
-      q = lane < kFinish / 32 ? sums[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    }
-  }
-  const float ls = logf(q.y);
-  if (t == 0) {
-    if (out.lse != nullptr) out.lse[p] = q.x + ls;
-    if (out.entropy != nullptr) out.entropy[p] = ls - __fdividef(q.z, q.y);
-    if (a.y != nullptr) {
-      const int y = __ldg(a.y + p);
-      const bool ok = y >= 0 && y < a.V;
-      if (!ok) record_status(ctl, kStatusBadTarget);
-      // against M before log S: z_y - lse would round away what large logits leave
-      if (out.logp != nullptr) out.logp[p] = ok ? (__ldcg(a.zy + p) - q.x) - ls : 0.f;
-    }
-  }
-  if (K > 0) {
-    const unsigned long long bound =
-        static_cast<unsigned long long>(
-            __reduce_min_sync(0xffffffffu, lane < kList ? group[lane] : 0xffffffffu)) << 32;
-#pragma unroll 1
-    for (int k = t; k < sets; k += kFinish) {
-      const unsigned long long e = tops[k];
-      if (e != 0 && e >= bound) cand[atomicAdd(&count[0], 1)] = e;
-    }
-    // ranks twice: of the first entries, then of all that can be among the K largest
-    constexpr int kAhead = list_batch(K);
-#pragma unroll 1
-    for (int round = 0; round < 2; ++round) {
-      __syncthreads();
-      const int n = count[round];
-#pragma unroll 1
-      for (int k = t; k < n; k += kFinish) {
-        const unsigned long long x = cand[k];
-        int r = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) r += cand[j] > x ? 1 : 0;
-        if (r < kList) first[r] = x;
-      }
-      __syncthreads();
-      if (round == 0) {
-        // cand from here on: the K first, and the further entries ahead of the last of them:
-        // several per list at a time, until no list's last one looked at is
-        if (t < kList && first[t] != 0) cand[atomicAdd(&count[1], 1)] = first[t];
-        const unsigned long long last = first[kList - 1];
-        const unsigned long long f = t < kList * kAhead ? first[t / (kAhead > 0 ? kAhead : 1)] : 0;
-        const int set = f != 0 ? StreamSplit{a.V, ctas, a.rows}.list_of(key_id(f)) : 0;
-        const float2* rest = a.rest + (static_cast<long long>(p) * sets + set) * (kList - 1) - 1;
-        bool more = kAhead > 0;
-#pragma unroll 1
-        for (int j0 = 1; j0 < kList && more; j0 += kAhead) {
-          const int j = j0 + t % (kAhead > 0 ? kAhead : 1);
-          bool take = false;
-          if (f != 0 && j < kList) {
-            const unsigned long long x = entry_key(__ldcg(rest + j));
-            take = x > last;
-            if (take) cand[atomicAdd(&count[1], 1)] = x;
-          }
-          more = __syncthreads_or(take && j + 1 - j0 == kAhead) != 0;
-        }
-      }
-    }
-    // `first` now holds the answer; where there are fewer logits than asked for, the rest is empty
-    if (t < out.n_top) {
-      const unsigned long long x = t < count[1] ? first[t] : 0;
-      out.top_ids[static_cast<long long>(p) * out.n_top + t] = x != 0 ? key_id(x) : -1;
-      out.top_logp[static_cast<long long>(p) * out.n_top + t] =
-          x != 0 ? (from_ordered(static_cast<uint32_t>(x >> 32)) - q.x) - ls : -INFINITY;
-    }
-  }
-}
-
 template <int NT, int K>
 cudaError_t stream_launch(const CUtensorMap& mW, const CUtensorMap& mH, const StreamArgs& a,
                           int grid, const DevCtl& ctl, cudaStream_t st) {
@@ -580,12 +457,8 @@ cudaError_t stream_by_positions(const CUtensorMap& mW, const CUtensorMap& mH, co
     default: e = stream_launch<64, K>(mW, mH, a, ctas, ctl, st); break;
   }
   if (e != cudaSuccess) return e;
-  // the same split of the SMs' memory as the kernel before: another split would wait for the SMs
-  // to drain and change over (140 us instead of 132 us for 48 positions with 20 alternatives)
-  e = cudaFuncSetAttribute(k_stats_stream_finish<K>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                           cudaSharedmemCarveoutMaxShared);
-  if (e != cudaSuccess) return e;
-  return launch_after(k_stats_stream_finish<K>, dim3(a.n), kFinish, st, a, ctas, out, ctl);
+  return launch_join<K>(StreamSets{a.part, a.top, a.rest, a.V, ctas, a.rows}, a.y, a.zy, a.n, a.V, out,
+                        ctl, st);
 }
 
 }  // namespace
