@@ -27,12 +27,11 @@ struct FwdArgs {
   uint8_t* scales;
 };
 
-// f = (f - mu) r w + b
-__device__ __forceinline__ void normed(float2 (&f)[4], float mu, float r, const float2 (&w)[4],
+// f = f r w + b, f centred
+__device__ __forceinline__ void normed(float2 (&f)[4], float r, const float2 (&w)[4],
                                        const float2 (&b)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    f[j] = __ffma2_rn(__fmul2_rn(__fadd2_rn(f[j], both(-mu)), both(r)), w[j], b[j]);
+  for (int j = 0; j < 4; ++j) f[j] = __ffma2_rn(__fmul2_rn(f[j], both(r)), w[j], b[j]);
 }
 
 // 1 / sqrt(v), v = spread / d + eps: the hardware's estimate (a few units off in the last place)
@@ -55,20 +54,20 @@ __global__ void __launch_bounds__(256) k_norm_fwd_short(Src x, Out y, FwdArgs a)
   const bool in = row < a.rows && col < a.d;
   float2 f[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
   if (in) Src::widen(x.load(row, col), f);
+  if (a.codes != nullptr)
+    hold8(f, a.codes, a.scales, row, col, a.d, a.blocks, in, G < 4 ? G : 4);
   const float inv_d = 1.f / static_cast<float>(a.d);
   const float mu = a.rms ? 0.f : lanes_total<G>(sum8(f)) * inv_d;
-  const float r = rstd_of(lanes_total<G>(in ? spread8(f, mu) : 0.f), inv_d, a.eps);
+  const float r = rstd_of(lanes_total<G>(in ? center8(f, mu) : 0.f), inv_d, a.eps);
   if (lane == 0 && in) {
     if (a.mean != nullptr) a.mean[row] = mu;
     if (a.rstd != nullptr) a.rstd[row] = r;
   }
-  if (a.codes != nullptr)
-    hold8(f, a.codes, a.scales, row, col, a.d, a.blocks, in, G < 4 ? G : 4);
   if (in) {
     float2 w[4], b[4];
     load_vec(a.weight, a.wbf16, col, 1.f, w);
     load_vec(a.bias, a.wbf16, col, 0.f, b);
-    normed(f, mu, r, w, b);
+    normed(f, r, w, b);
     y.store(row, col, f);
   }
 }
@@ -127,6 +126,13 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_rows(Src x, Out y, FwdArg
     }
     __syncwarp();
     fetch(row + step);                                  // the slot is read: refill it
+    if (a.codes != nullptr) {
+#pragma unroll
+      for (int u = 0; u < NV; ++u) {
+        const int col = (u * kLanes + gl) * 8;
+        hold8(f[u], a.codes, a.scales, row, col, a.d, a.blocks, col < a.d);
+      }
+    }
     float mu = 0.f;
     if (!a.rms) {
       float s = 0.f;
@@ -138,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_rows(Src x, Out y, FwdArg
     float q = 0.f;
 #pragma unroll
     for (int u = 0; u < NV; ++u)
-      if ((u * kLanes + gl) * 8 < a.d) q += spread8(f[u], mu);
+      if (u * kLanes + gl < vecs) q += center8(f[u], mu);
     const float r = rstd_of(group_total<WG>(q, &red[turn][group * WG], group, wg, lane), inv_d,
                             a.eps);
     turn ^= 1;
@@ -149,13 +155,11 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_rows(Src x, Out y, FwdArg
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int col = (u * kLanes + gl) * 8;
-      const bool in = col < a.d;
-      if (a.codes != nullptr) hold8(f[u], a.codes, a.scales, row, col, a.d, a.blocks, in);
-      if (in) {
+      if (col < a.d) {
         float2 w[4], b[4];
         sw.load(u * kLanes + gl, w);
         sb.load(u * kLanes + gl, b);
-        normed(f[u], mu, r, w, b);
+        normed(f[u], r, w, b);
         y.store(row, col, f[u]);
       }
     }
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(Src x, Out y, Fw
   for (int col = threadIdx.x * 8; col < a.d; col += kWideThreads * 8) {
     float2 f[4];
     Src::widen(x.load(row, col), f);
-    q += spread8(f, mu);
+    q += center8(f, mu);
   }
   const float r = rstd_of(block_total(q, buf), inv_d, a.eps);
   if (threadIdx.x == 0) {
@@ -200,7 +204,8 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(Src x, Out y, Fw
       float2 w[4], b[4];
       load_vec(a.weight, a.wbf16, col, 1.f, w);
       load_vec(a.bias, a.wbf16, col, 0.f, b);
-      normed(f, mu, r, w, b);
+      center8(f, mu);
+      normed(f, r, w, b);
       y.store(row, col, f);
     }
   }

@@ -21,13 +21,13 @@ __device__ __forceinline__ float sum8(const float2 (&f)[4]) {
   const float2 s = __fadd2_rn(__fadd2_rn(f[0], f[1]), __fadd2_rn(f[2], f[3]));
   return s.x + s.y;
 }
-// sum of (f - mu)^2
-__device__ __forceinline__ float spread8(const float2 (&f)[4], float mu) {
+// f -= mu, and the sum of its squares
+__device__ __forceinline__ float center8(float2 (&f)[4], float mu) {
   float2 q = both(0.f);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 c = __fadd2_rn(f[j], both(-mu));
-    q = __ffma2_rn(c, c, q);
+    f[j] = __fadd2_rn(f[j], both(-mu));
+    q = __ffma2_rn(f[j], f[j], q);
   }
   return q.x + q.y;
 }

@@ -82,10 +82,10 @@ __device__ __forceinline__ bool warps_all(bool mine) {
   return all != 0;
 }
 
-// Long lists: a new logit costs a pass over the list, 12 us for the first tile and 38 us for the
-// eight after it at K = 32 and 48 positions. Bids between the CTAs, as the GEMM route's tiles make
-// them (stats.cu), leave the eight 9 us. Lists of 8 cost 16 us in all without, and the bids' zeroing
-// a launch; they have none.
+// Long lists: a new logit costs a pass over the list. At K = 32 and 48 positions the first of nine
+// tiles takes the position warps 12 us and the others 38 us together; with bids between the CTAs,
+// as the GEMM route's tiles make them (stats.cu), 14 us and 17 us (a tile arrives every 10 us).
+// Lists of 8 take 5 us and 13 us without; they have none, and no launch that zeroes them.
 constexpr int kBidGroups = 32;
 constexpr bool has_bids(int K) { return K >= kBidGroups; }
 
