@@ -4,7 +4,9 @@
 //                    vocabulary tile, the running maximum m, S = sum e^(z-m),
 //                    T = sum e^(z-m) (z-m), the target logit and the tile's K largest logits
 //   k_stats_f32<K>   the same partials on the fp32 SIMT route
-//   k_stats_finish<K>  one warp per position: joins the tiles
+//   k_stats_join<K>  joins the tiles, a block per position (stats_join.cuh), or
+//   k_stats_finish<K>  a warp per position: many positions, or very many tiles
+// Up to 64 bf16 positions stream W instead (stats_stream.cu).
 //
 // Entropy: -sum p log p = log S - T / S. Both terms are >= 0 (T <= 0), so the sum does not
 // cancel, and T rescales with the maximum like S does: moving from m to m' multiplies both
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(256) k_stats_finish(const float2* __restrict__
   const double ls = log(a.s);
   if (lane == 0) {
     if (out.lse != nullptr) out.lse[i] = static_cast<float>(a.M + ls);
-    if (out.entropy != nullptr) out.entropy[i] = static_cast<float>(ls - a.t / a.s);
+    if (out.entropy != nullptr) out.entropy[i] = entropy_of(static_cast<float>(ls - a.t / a.s));
     if (y != nullptr) {
       const int yi = __ldcg(y + i);
       const bool ok = yi >= 0 && yi < V;

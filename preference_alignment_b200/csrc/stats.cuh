@@ -24,6 +24,9 @@ __device__ __forceinline__ float from_ordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
+// Rounding can leave an entropy of 0 a little below it (NaN stays NaN).
+__device__ __forceinline__ float entropy_of(float e) { return e < 0.f ? 0.f : e; }
+
 // ------------------------------------------------------------------ lists across a warp
 // A falling list of 32 (logit, id) entries, entry j in lane j.
 struct Entry {

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kJoin) k_stats_join(Sets sets, const int* y, c
   const float ls = logf(q.y);
   if (t == 0) {
     if (out.lse != nullptr) out.lse[p] = q.x + ls;
-    if (out.entropy != nullptr) out.entropy[p] = ls - __fdividef(q.z, q.y);
+    if (out.entropy != nullptr) out.entropy[p] = entropy_of(ls - __fdividef(q.z, q.y));
     if (y != nullptr) {
       const int yp = __ldcg(y + p);
       const bool ok = yp >= 0 && yp < V;

@@ -7,8 +7,12 @@
 // tile t going to CTA t mod gridDim, in tiles of at most 128 rows so many that every CTA gets the
 // same number (V = 151,936: 9 tiles of 115 rows on each of 148 CTAs; with 128 rows, 3 tiles would
 // make a ninth wave). (One contiguous range per CTA reads 148 places of W at a time instead of
-// one: 187 us instead of 164 us at V = 128,256, d = 4096.) Every running value stays on chip until the CTA is done, so a position leaves one set
-// of sums per CTA, not one per tile.
+// one: 187 us instead of 164 us at V = 128,256, d = 4096.) Every running value stays on chip until
+// the CTA is done, so a position leaves one set of sums per CTA, not one per tile.
+//
+// HBM bounds it: one position at V = 128,256, d = 4096 takes 158 us (6.6 TB/s), with 8 alternatives
+// and the join 168 us; 48 positions at V = 151,936, d = 2048 take 103 us, 110 us with 8
+// alternatives, 125 us with 20 (the lists' upkeep, see kBidGroups).
 //
 // Roles (320 threads): warp 0 issues the TMA loads, warp 1 owns TMEM and issues the MMAs, warps
 // 2-9 turn the accumulator around through shared memory (z[position][vocabulary row]); then each
@@ -330,13 +334,16 @@ __global__ void __launch_bounds__(kSThreads, 1)
       tt = f * fmaf(s, back, tt);
       s *= f;
       m = nm;
+      float ds = 0.f, dt = 0.f;              // the tile's own sums: short chains of additions
 #pragma unroll
       for (int j = 0; j < kSegRows; ++j) {
         const float b = fmaf(x[j], kLog2eS, -nref);
         const float ex = ex2_approx(b);
-        s += ex;
-        tt = fmaf(ex, fmaxf(b, -1e30f), tt);               // the bound keeps 0 * -inf out of T
+        ds += ex;
+        dt = fmaf(ex, fmaxf(b, -1e30f), dt);               // the bound keeps 0 * -inf out of T
       }
+      s += ds;
+      tt += dt;
       if (K > 0) {
         // K / 4 logits of each of the position's 4 threads are K logits: one below the smallest of
         // their (K / 4)-th is no alternative (nor one equal to it: its id would be the highest)

@@ -116,6 +116,9 @@ CASES = [  # n, d, V, n_top
     (255, 64, 300, 2), (257, 128, 2050, 8), (300, 1024, 1300, 32), (700, 64, 260, 3),
     (16, 72, 1184, 8), (17, 64, 9, 20), (32, 64, 19001, 8), (64, 64, 60001, 20), (64, 320, 2368, 32),
     (65, 64, 3000, 8), (2, 64, 130000, 32), (50, 8, 40007, 1),
+    (3, 65536, 300, 8), (70, 16384, 260, 8),
+    # more tiles than the block join takes (1,024), and more positions (1,024): the warp join
+    (70, 8, 300001, 8), (3, 8, 33100, 20), (1100, 16, 700, 32), (1100, 16, 700, 1), (1030, 8, 300, 0),
 ]
 
 
@@ -141,9 +144,10 @@ def test_rows_exact_ids_on_a_grid(n, d, V, n_top, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n_top", [1, 8, 32])
-def test_equal_logits_come_by_id(n_top, dtype):
+@pytest.mark.parametrize("n,V", [(40, 3001), (90, 3001), (1100, 900), (3, 40000)])
+def test_equal_logits_come_by_id(n, V, n_top, dtype):
     """All logits equal: every tile's list is full of ties; and two levels only."""
-    n, d, V = 40, 64, 3001
+    d = 64
     h = WL.encode(np.ones((n, d), np.float32), dtype)
     W = np.zeros((V, d), np.float32)
     o = run_rows(h, WL.encode(W, dtype), dtype, [0] * n, n_top)
@@ -157,12 +161,13 @@ def test_equal_logits_come_by_id(n_top, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rising", [True, False])
-def test_sorted_vocabulary(rising, dtype):
+@pytest.mark.parametrize("n,V,n_top", [(130, 2900, 8), (5, 2900, 32), (20, 4000, 8), (1030, 1100, 32)])
+def test_sorted_vocabulary(n, V, n_top, rising, dtype):
     """Logits that rise along the vocabulary renew the alternatives in every tile; falling ones
     never after the first."""
-    n, d, V, n_top = 130, 8, 2900, 8
+    d = 8
     h = np.zeros((n, d), np.float32)
-    h[:, 0], h[:, 1] = 1.0, 16.0                       # z = a + 16 b: V distinct values, exact
+    h[:, 0], h[:, 1] = 1.0, 16.0                       # z = a + 16 b, a < 16, b < 256: distinct, exact
     v = np.arange(V) if rising else np.arange(V)[::-1]
     W = np.zeros((V, d), np.float32)
     W[:, 0], W[:, 1] = (v % 16) / 32.0, (v // 16) / 32.0
@@ -378,3 +383,19 @@ def test_gemm_kernels_agree():
             check(g, o, 20, 0.0, exact_ids=True)
         finally:
             libdpo.set_gemm_variant(old)
+
+
+def test_largest_vocabulary():
+    """2^24 rows: every CTA walks 886 tiles, ids pass 2^24 - 256."""
+    import torch
+    n, d, V, n_top = 2, 8, 1 << 24, 8
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    W = (torch.randint(-128, 128, (V, d), generator=gen, device="cuda") / 64).bfloat16()   # exact
+    H = (torch.randint(-8, 8, (n, d), generator=gen, device="cuda") / 4).bfloat16()
+    t = torch.tensor([V - 1, 0], dtype=torch.int32, device="cuda")
+    g = Got(n, n_top)
+    libdpo.token_stats_rows(H, W, t, n_top, ws=_space(libdpo.token_stats_rows_size(n, d, V, n_top)[0]),
+                            **g.args())
+    assert libdpo.check() == libdpo.OK
+    check(g, HO.token_stats(np64(H), np64(W), t.cpu().numpy(), n_top), n_top, 0.0, exact_ids=True)
