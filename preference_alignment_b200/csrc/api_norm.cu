@@ -1,5 +1,6 @@
 // C ABI of the norm before the head and of 8-bit activation checkpoints: argument checks and
 // launches. See include/dpo.h for the contract of every call.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -49,8 +50,9 @@ struct Span {
 // Checks a row buffer and describes it.
 dpo_status rows_ok(const void* p, int32_t dtype, int32_t rows, int32_t d, int64_t stride,
                    Span* out) {
-  // the bound keeps rows * stride within 64 bits
-  if (p == nullptr || stride < d || stride > (1ll << 28)) return DPO_ERR_INVALID_ARG;
+  // the bound keeps rows * stride in bytes within 64 bits, far above what memory holds
+  if (p == nullptr || stride < d || stride > (1ll << 60) / std::max(rows, 1))
+    return DPO_ERR_INVALID_ARG;
   if (stride % 8 != 0) return DPO_ERR_UNSUPPORTED;
   if (!aligned16(p)) return DPO_ERR_INVALID_ARG;
   out->begin = reinterpret_cast<uintptr_t>(p);
