@@ -412,7 +412,7 @@ cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const S
                        int V, int d, const int* y, int sms, int* sync, const DevCtl& ctl,
                        cudaStream_t st) {
   if (K > 0) {
-    const cudaError_t e = 
+    const cudaError_t e =
         cudaMemsetAsync(b.tau, 0, sizeof(uint32_t) * static_cast<size_t>(K) * b.ldp, st);
     if (e != cudaSuccess) return e;
   }
@@ -423,7 +423,6 @@ cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const S
 
 template <int K>
 cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, const int* y,
-                        
                          const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
   const uint32_t* tau = with_tau ? b.tau : nullptr;
   if (n <= kBlockJoin && S <= kJoinSets)

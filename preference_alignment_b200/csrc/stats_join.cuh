@@ -156,17 +156,22 @@ __global__ void __launch_bounds__(kJoin) k_stats_join(Sets sets, const int* y, c
         const unsigned long long last =
             kFrom > 0 ? first[kList - 1] + 1 : first[kList - 1] >> 32 << 32;
         if (kFrom > 0 && t < kList && first[t] != 0) cand[atomicAdd(&count[1], 1)] = first[t];
-        bool more = kBatch > 0;
+        bool open = f != 0, more = kBatch > 0;
 #pragma unroll 1
         for (int j0 = kFrom; j0 < kList && more; j0 += kBatch) {
           const int j = j0 + t % (kBatch > 0 ? kBatch : 1);
           bool take = false;
-          if (f != 0 && j < kList) {
+          if (open && j < kList) {
             const unsigned long long x = entry_key(sets.template entry<kList>(p, f, j));
             take = x != 0 && x >= last;
             if (take) cand[atomicAdd(&count[1], 1)] = x;
           }
-          more = __syncthreads_or(take && j + 1 - j0 == kBatch) != 0;
+          if constexpr (kList - kFrom > kBatch) {
+            // each list by itself: behind a batch that is not full nothing was written
+            static_assert(kBatch > 0 && 32 % kBatch == 0, "a list's threads are in one warp");
+            open = (__ballot_sync(0xffffffffu, take) >> (lane | (kBatch - 1)) & 1) != 0;
+            more = __syncthreads_or(open) != 0;
+          }
         }
       }
     }

@@ -399,3 +399,31 @@ def test_largest_vocabulary():
                             **g.args())
     assert libdpo.check() == libdpo.OK
     check(g, HO.token_stats(np64(H), np64(W), t.cpu().numpy(), n_top), n_top, 0.0, exact_ids=True)
+
+
+@pytest.mark.parametrize("n_top", [4, 8, 20, 32])
+@pytest.mark.parametrize("n", [16, 64])
+def test_equal_logits_across_the_tiles_of_a_cta(n, n_top):
+    """Levels of equal logits that fill up over two tiles of 128 rows: those of the later tile come by
+    id, whichever segment of it is worked on first. Position p has its largest ones in CTA 2 p's tiles,
+    in lists of very different lengths."""
+    import torch
+    d, tiles, ctas, rows = 64, 6, 148, 128
+    V = rows * tiles * ctas
+    v = np.arange(V)
+    # one workspace: what an earlier call left there counts for nothing
+    ws = torch.empty(libdpo.token_stats_rows_size(n, d, V, n_top)[0], dtype=torch.uint8, device="cuda")
+    for seed in range(8):
+        rng = np.random.default_rng(seed)
+        level = v // (rows * ctas) // 2
+        z = np.where(rng.random((V, d)) < 0.05 * (1 + seed % 3), level[:, None] + 1, 0).astype(np.float32)
+        z[(v[:, None] // rows) % ctas == 2 * np.arange(d)[None, :]] += 8
+        H = torch.eye(d, dtype=torch.bfloat16, device="cuda")[:n]      # position p's logits: column p
+        ids = torch.empty(n, n_top, dtype=torch.int32, device="cuda")
+        top = torch.empty(n, n_top, device="cuda")
+        W = torch.from_numpy(z).cuda().bfloat16()
+        want = np.stack([np.lexsort((v, -z[:, p]))[:n_top] for p in range(n)])
+        for _ in range(5):
+            libdpo.token_stats_rows(H, W, None, n_top, top_ids=ids, top_logp=top, ws=ws)
+            assert np.array_equal(ids.cpu().numpy(), want)
+    assert libdpo.check() == libdpo.OK
