@@ -39,7 +39,7 @@ struct StreamShape {
   static constexpr int kPitch = kSRows + 1;                // of z: odd, so columns spread over banks
   static constexpr int kZ = NT * kPitch * 4;               // z[position][row], later the sums
   static constexpr int kSmem =
-      kStages * kStage + kZ + NT * 4 + 2 * kSSegs * NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
+      kStages * kStage + kZ + NT * 4 + 3 * kSSegs * NT * 4 + (2 * kStages + 5) * 8 + 16 + 1024;
   static constexpr int kTmem = 2 * NT < 32 ? 32 : 2 * NT;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
 };
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
   uint8_t* sH = sW + kStages * kSWBytes;
   float* z = reinterpret_cast<float*>(sH + kStages * Sh::kHBytes);
   int* sy = reinterpret_cast<int*>(z + NT * Sh::kPitch);
-  float* share = reinterpret_cast<float*>(sy + NT);    // [kSSegs][NT]
-  uint32_t* bound = reinterpret_cast<uint32_t*>(share + kSSegs * NT);   // [kSSegs][NT] of the bids
+  float* share = reinterpret_cast<float*>(sy + NT);    // [2][kSSegs][NT], by the tile's parity
+  uint32_t* bound = reinterpret_cast<uint32_t*>(share + 2 * kSSegs * NT);   // [kSSegs][NT] of the bids
   uint64_t* bars = reinterpret_cast<uint64_t*>(bound + kSSegs * NT);
   // bars: [0, S) full, [S, 2S) empty, 2S + {0,1} acc_full, 2S + {2,3} acc_empty, 2S + 4 drain
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 5);
@@ -349,9 +349,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
         // their (K / 4)-th is no alternative (nor one equal to it: its id would be the highest)
         float low = val[kList - 1];
         if (K >= kSSegs && t > 0 && mine) {
-          float all = share[p];
+          const float* last = share + ((t - 1) & 1) * kSSegs * NT;
+          float all = last[p];
 #pragma unroll
-          for (int g = 1; g < kSSegs; ++g) all = fminf(all, share[g * NT + p]);
+          for (int g = 1; g < kSSegs; ++g) all = fminf(all, last[g * NT + p]);
           low = fmaxf(low, all);
         }
         float tauv = -INFINITY;
@@ -375,8 +376,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
           bid = val[0];
           atomicMax(a.bids + blockIdx.x % kBidGroups * a.n + p, ordered(bid));
         }
-        // read after the next tile's barrier
-        if (K >= kSSegs && mine) share[seg * NT + p] = val[kList >= kSSegs ? kList / kSSegs - 1 : 0];
+        // read after the next tile's barrier; not in the place that the last tile's are read from:
+        // this tile's logits have higher ids in other segments
+        if (K >= kSSegs && mine)
+          share[((t & 1) * kSSegs + seg) * NT + p] = val[kList >= kSSegs ? kList / kSSegs - 1 : 0];
       }
     }
     // a position's segments join in a fixed order, in z's place; one set of sums per CTA
@@ -405,9 +408,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
         // goes on to the next only from a full one
         float low = kFloor;
         if (K >= kSSegs) {
-          low = share[p];
+          const float* last = share + ((tiles - 1) & 1) * kSSegs * NT;
+          low = last[p];
 #pragma unroll
-          for (int g = 1; g < kSSegs; ++g) low = fminf(low, share[g * NT + p]);
+          for (int g = 1; g < kSSegs; ++g) low = fminf(low, last[g * NT + p]);
         }
         float2* l = a.rest + at * (kList - 1);
         bool open = true;
