@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) k_norm_fwd_short(Src x, Out y, FwdArgs a)
   float2 f[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
   if (in) Src::widen(x.load(row, col), f);
   if (a.codes != nullptr)
-    hold8(f, a.codes, a.scales, row, col, a.d, a.blocks, in, G < 4 ? G : 4);
+    hold8(f, Held(a.codes, a.scales, row, col, a.d, a.blocks), in, G < 4 ? G : 4);
   const float inv_d = 1.f / static_cast<float>(a.d);
   const float mu = a.rms ? 0.f : lanes_total<G>(sum8(f)) * inv_d;
   const float r = rstd_of(lanes_total<G>(in ? center8(f, mu) : 0.f), inv_d, a.eps);
@@ -127,11 +127,10 @@ __global__ void __launch_bounds__(kThreads) k_norm_fwd_rows(Src x, Out y, FwdArg
     __syncwarp();
     fetch(row + step);                                  // the slot is read: refill it
     if (a.codes != nullptr) {
+      const Held to(a.codes, a.scales, row, gl * 8, a.d, a.blocks);
 #pragma unroll
-      for (int u = 0; u < NV; ++u) {
-        const int col = (u * kLanes + gl) * 8;
-        hold8(f[u], a.codes, a.scales, row, col, a.d, a.blocks, col < a.d);
-      }
+      for (int u = 0; u < NV; ++u)
+        hold8(f[u], to.right(u * kLanes * 8), u * kLanes + gl < vecs);
     }
     float mu = 0.f;
     if (!a.rms) {
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(Src x, Out y, Fw
     const bool in = col < a.d;
     float2 f[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
     if (in) Src::widen(x.load(row, col), f);
-    if (a.codes != nullptr) hold8(f, a.codes, a.scales, row, col, a.d, a.blocks, in);
+    if (a.codes != nullptr) hold8(f, Held(a.codes, a.scales, row, col, a.d, a.blocks), in);
     if (in) {
       float2 w[4], b[4];
       load_vec(a.weight, a.wbf16, col, 1.f, w);

@@ -92,7 +92,7 @@ __device__ __forceinline__ float block_total(float x, float* buf) {
 }
 
 constexpr int kWideThreads = 512;
-constexpr int kSmemBytes = 220 * 1024;    // dynamic shared memory a block may ask for
+constexpr int kSmemBytes = 226 * 1024;    // dynamic shared memory a block may ask for
 
 inline int short_lanes(int d) {
   int g = 1;

@@ -119,8 +119,10 @@ __global__ void __launch_bounds__(kShortThreads) k_norm_bwd_short(X x, Dy dy, Dx
 // Groups of WG warps per row, NV groups of 8 values per lane (see the forward): a lane's columns
 // stay the same from row to row, so the weight gradients gather in its registers; the block's
 // groups add theirs up at the end and leave one partial gradient. Two slots per group: while a
-// row is worked on, the next two are on their way.
+// row is worked on, the next two are on their way. Rows of more than 2 groups a lane leave no
+// registers for g: they read dy again from the slot, which is then refilled a little later.
 constexpr int kSlots = 2;
+constexpr bool holds_g(int nv) { return nv <= 2; }
 
 template <class X, class Dy, class Dx, int NV, int WG, int kThreads, bool kMean>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, BwdArgs a) {
@@ -176,30 +178,36 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
     cp_async_wait<kSlots - 1>();
     __syncwarp();
     const float mu2 = kMean ? stat(a.mean, row + step) : 0.f, rs2 = stat(a.rstd, row + step);
-    float2 f[NV][4], e[NV][4];
+    constexpr bool kHold = holds_g(NV);
+    float2 f[NV][4], e[kHold ? NV : 1][4];
     float c1 = 0.f, c2 = 0.f;
+    auto terms = [&](int u, int k, float2 (&dyv)[4]) {
+      float2 w[4];
+      sw.load(k, w);
+      float p1, p2;
+      grad_terms<kMean>(f[u], dyv, mu, rs, w, aw[u], ab[u], p1, p2);
+      c1 += p1;
+      c2 += p2;
+    };
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
       const int k = u * kLanes + gl;
       if (k < vecs) {
-        Dy::widen(Dy::take(slot, k, {}), e[u]);
+        float2 (&dyv)[4] = e[kHold ? u : 0];
+        Dy::widen(Dy::take(slot, k, {}), dyv);
         X::widen(X::take(slot + kSlotDy, k, side[u]), f[u]);
+        if (!kHold) terms(u, k, dyv);
       }
     }
-    __syncwarp();
-    fetch(row + 2 * step, slot);                        // the slot is read: refill it
+    if (kHold) {
+      __syncwarp();
+      fetch(row + 2 * step, slot);                      // the slot is read: refill it
+    }
     sides(row + step);
+    if (kHold) {
 #pragma unroll
-    for (int u = 0; u < NV; ++u) {
-      const int k = u * kLanes + gl;
-      if (k < vecs) {
-        float2 w[4];
-        sw.load(k, w);
-        float p1, p2;
-        grad_terms<kMean>(f[u], e[u], mu, rs, w, aw[u], ab[u], p1, p2);
-        c1 += p1;
-        c2 += p2;
-      }
+      for (int u = 0; u < NV; ++u)
+        if (u * kLanes + gl < vecs) terms(u, u * kLanes + gl, e[kHold ? u : 0]);
     }
     c1 = kMean ? lanes_total(c1) : 0.f;
     c2 = lanes_total(c2);
@@ -223,10 +231,22 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
       for (int u = 0; u < NV; ++u) {
         const int k = u * kLanes + gl;
         if (k < vecs) {
-          grad_x<kMean>(f[u], e[u], rs, c1 * inv_d, c2 * inv_d);
+          float2 (&g)[4] = e[kHold ? u : 0];
+          if (!kHold) {
+            float2 w[4];
+            sw.load(k, w);
+            Dy::widen(Dy::take(slot, k, {}), g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(g[j], w[j]);
+          }
+          grad_x<kMean>(f[u], g, rs, c1 * inv_d, c2 * inv_d);
           dx.store(row, k * 8, f[u]);
         }
       }
+    }
+    if (!kHold) {
+      __syncwarp();
+      fetch(row + 2 * step, slot);
     }
     mu = mu2;
     rs = rs2;
@@ -372,6 +392,7 @@ __global__ void __launch_bounds__(256) k_norm_dw_sum(const float* pw, const floa
   }
 }
 
+constexpr int kMaxShort = 128;
 constexpr int kWideSplits = 32;
 constexpr int kMaxBwd = 8192;           // longest row of the groups: 8 warps of 4 groups a lane
 
@@ -380,7 +401,7 @@ constexpr int kMaxBwd = 8192;           // longest row of the groups: 8 warps of
 template <class X, class Dy, class Dx, int NV, int WG, bool kMean>
 cudaError_t bwd_rows(const X& x, const Dy& dy, const Dx& dx, const BwdArgs& a, int* parts, int sms,
                      cudaStream_t st) {
-  constexpr int kThreads = NV > 2 ? 384 : 512;
+  constexpr int kThreads = NV == 1 ? 1024 : 512;
   auto kern = k_norm_bwd_rows<X, Dy, Dx, NV, WG, kThreads, kMean>;
   const size_t vec = sizeof(float) * static_cast<size_t>(a.d);
   const size_t slots = static_cast<size_t>(kSlots) * NV * WG * 32 * (X::kSlot + Dy::kSlot);
@@ -398,10 +419,12 @@ cudaError_t bwd_rows(const X& x, const Dy& dy, const Dx& dx, const BwdArgs& a, i
 template <class X, class Dy, class Dx, bool kMean>
 cudaError_t bwd_by_length(const X& x, const Dy& dy, const Dx& dx, const BwdArgs& a, int* parts,
                           int sms, cudaStream_t st) {
+  if (a.d <= 256) return bwd_rows<X, Dy, Dx, 1, 1, kMean>(x, dy, dx, a, parts, sms, st);
   if (a.d <= 512) return bwd_rows<X, Dy, Dx, 2, 1, kMean>(x, dy, dx, a, parts, sms, st);
   if (a.d <= 1024) return bwd_rows<X, Dy, Dx, 2, 2, kMean>(x, dy, dx, a, parts, sms, st);
   if (a.d <= 2048) return bwd_rows<X, Dy, Dx, 2, 4, kMean>(x, dy, dx, a, parts, sms, st);
   if (a.d <= 4096) return bwd_rows<X, Dy, Dx, 2, 8, kMean>(x, dy, dx, a, parts, sms, st);
+  if (a.d <= 6144) return bwd_rows<X, Dy, Dx, 3, 8, kMean>(x, dy, dx, a, parts, sms, st);
   return bwd_rows<X, Dy, Dx, 4, 8, kMean>(x, dy, dx, a, parts, sms, st);
 }
 
@@ -433,7 +456,7 @@ cudaError_t norm_bwd(const X& x, const Dy& dy, const Dx& dx, BwdArgs a, float* w
       k_norm_dw_wide<<<dim3((a.d + 255) / 256, parts), 256, 0, st>>>(x, dy, a);
     if (dx.p != nullptr) k_norm_dx_wide<<<a.rows, kWideThreads, 0, st>>>(x, dy, dx, a);
     e = cudaGetLastError();
-  } else if (a.d <= 256) {
+  } else if (a.d <= kMaxShort) {
     const int rows_at_once = kShortThreads / short_lanes(a.d);
     parts = std::min(std::min(4 * sms, norm_parts(a.d)), (a.rows + rows_at_once - 1) / rows_at_once);
     e = bwd_short(x, dy, dx, a, parts, st);
@@ -460,7 +483,7 @@ cudaError_t norm_bwd_dy(const X& x, const NormGradBuf& g, const Dx& dx, const Bw
 }  // namespace
 
 // One partial per SM; short rows take several blocks of 256 threads per SM.
-int norm_parts(int d) { return d > kMaxBwd ? kWideSplits : d <= 256 ? 4 * kPlanSms : kPlanSms; }
+int norm_parts(int d) { return d > kMaxBwd ? kWideSplits : d <= kMaxShort ? 4 * kPlanSms : kPlanSms; }
 
 cudaError_t launch_norm_bwd(const NormIn& n, const NormGradBuf& g, int sms, cudaStream_t st) {
   const BwdArgs a{n.rows, n.d, n.wbf16, n.weight, g.mean, g.rstd, nullptr, nullptr};
