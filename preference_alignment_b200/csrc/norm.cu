@@ -7,10 +7,14 @@
 //   dx = r (g - c1 - xh c2), g = dy w, c1 = mean g (rms: 0), c2 = mean(g xh)
 //   dw = sum over rows of dy xh, db = sum over rows of dy
 //
+// The forward is bounded as much by its instructions, about 80 per 8 values, as by HBM: 16,384 rows
+// of 4,096 in bf16 take 45.5 us (5.9 TB/s), 62 us when they are held in 8 bits too.
+//
 // Forms by the row's length d, each row read once except in the last:
-//   d <= 256     a few lanes per row, one group of 8 values per lane
-//   d <= 16384   groups of 1 to 8 warps per row, the row in registers
-//   above        a block per row that reads it again (from L2) instead of holding it
+//   d <= 256     a few lanes per row, one group of 8 values per lane (16,384 rows of 256: 5.1 us, a
+//                warp per row 6.5 us; 262,144 rows: 68 us and 65 us)
+//   d <= 16384   groups of 1 to 8 warps per row, the row in registers (4,096 rows of 16,384: 48 us)
+//   above        a block per row that reads it again (from L2) instead of holding it (61 us there)
 // The backward is in norm_bwd.cu.
 #include "norm.cuh"
 

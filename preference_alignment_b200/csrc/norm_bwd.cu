@@ -1,8 +1,14 @@
 // The norm's backward (see norm.cu for the formulas): x and dy are read once and dx written once,
-// so HBM bounds it; the weight gradients gather on chip and leave one partial row per block.
-//   d <= 256   a few lanes per row, one group of 8 values per lane
-//   d <= 8192  groups of 1 to 8 warps per row
-//   above      a block per row that reads it twice, and a column sum that reads it again
+// so HBM bounds it; the weight gradients gather on chip and leave one partial row per block, which
+// k_norm_dw_sum adds up in a fixed order. 16,384 rows of 4,096, bf16 x, fp32 dy, both weight
+// gradients: 82 us (6.5 TB/s), 85 us in calls one after another; bf16 dy 70 us.
+// By the row's length d (times with the weight gradients, bf16 x, fp32 dy):
+//   d <= 128   a few lanes per row, one group of 8 values per lane (262,144 rows of 128: 58 us, a
+//              warp per row 73 us; of 256: 113 us and 90 us)
+//   d <= 8192  groups of 1 to 8 warps per row (8,192 rows of 8,192: 95 us; as below 168 us)
+//   above      a block per row that reads it twice, and a column sum that reads it again: the weight
+//              gradients of a row of 16,384 no longer fit the registers and shared memory of an SM
+//              beside two rows (4,096 rows of 16,384: 158 us, half the rate)
 #include "chain.cuh"
 #include "norm.cuh"
 
@@ -119,10 +125,13 @@ __global__ void __launch_bounds__(kShortThreads) k_norm_bwd_short(X x, Dy dy, Dx
 // Groups of WG warps per row, NV groups of 8 values per lane (see the forward): a lane's columns
 // stay the same from row to row, so the weight gradients gather in its registers; the block's
 // groups add theirs up at the end and leave one partial gradient. Two slots per group: while a
-// row is worked on, the next two are on their way. Rows of more than 2 groups a lane leave no
-// registers for g: they read dy again from the slot, which is then refilled a little later.
+// row is worked on, the next two are on their way. More than 2 groups a lane leave no registers
+// for g, more than 3 none for xh either: those are formed again from the slot, which is then
+// refilled a little later. (8,192 rows of 8,192: 95 us; with xh kept 116 us, with both and 384
+// threads 115 us.)
 constexpr int kSlots = 2;
 constexpr bool holds_g(int nv) { return nv <= 2; }
+constexpr bool holds_xh(int nv) { return nv <= 3; }
 
 template <class X, class Dy, class Dx, int NV, int WG, int kThreads, bool kMean>
 __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, BwdArgs a) {
@@ -179,13 +188,14 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
     __syncwarp();
     const float mu2 = kMean ? stat(a.mean, row + step) : 0.f, rs2 = stat(a.rstd, row + step);
     constexpr bool kHold = holds_g(NV);
-    float2 f[NV][4], e[kHold ? NV : 1][4];
+    constexpr bool kHoldX = holds_xh(NV);
+    float2 f[kHoldX ? NV : 1][4], e[kHold ? NV : 1][4];
     float c1 = 0.f, c2 = 0.f;
     auto terms = [&](int u, int k, float2 (&dyv)[4]) {
       float2 w[4];
       sw.load(k, w);
       float p1, p2;
-      grad_terms<kMean>(f[u], dyv, mu, rs, w, aw[u], ab[u], p1, p2);
+      grad_terms<kMean>(f[kHoldX ? u : 0], dyv, mu, rs, w, aw[u], ab[u], p1, p2);
       c1 += p1;
       c2 += p2;
     };
@@ -195,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
       if (k < vecs) {
         float2 (&dyv)[4] = e[kHold ? u : 0];
         Dy::widen(Dy::take(slot, k, {}), dyv);
-        X::widen(X::take(slot + kSlotDy, k, side[u]), f[u]);
+        X::widen(X::take(slot + kSlotDy, k, side[u]), f[kHoldX ? u : 0]);
         if (!kHold) terms(u, k, dyv);
       }
     }
@@ -203,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
       __syncwarp();
       fetch(row + 2 * step, slot);                      // the slot is read: refill it
     }
-    sides(row + step);
+    if (kHoldX) sides(row + step);
     if (kHold) {
 #pragma unroll
       for (int u = 0; u < NV; ++u)
@@ -239,8 +249,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
 #pragma unroll
             for (int j = 0; j < 4; ++j) g[j] = __fmul2_rn(g[j], w[j]);
           }
-          grad_x<kMean>(f[u], g, rs, c1 * inv_d, c2 * inv_d);
-          dx.store(row, k * 8, f[u]);
+          float2 (&xh)[4] = f[kHoldX ? u : 0];
+          if (!kHoldX) {
+            X::widen(X::take(slot + kSlotDy, k, side[u]), xh);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              xh[j] = __fmul2_rn(kMean ? __fadd2_rn(xh[j], both(-mu)) : xh[j], both(rs));
+          }
+          grad_x<kMean>(xh, g, rs, c1 * inv_d, c2 * inv_d);
+          dx.store(row, k * 8, xh);
         }
       }
     }
@@ -248,6 +265,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
       __syncwarp();
       fetch(row + 2 * step, slot);
     }
+    if (!kHoldX) sides(row + step);
     mu = mu2;
     rs = rs2;
     turn ^= 1;
@@ -396,8 +414,11 @@ constexpr int kMaxShort = 128;
 constexpr int kWideSplits = 32;
 constexpr int kMaxBwd = 8192;           // longest row of the groups: 8 warps of 4 groups a lane
 
-// Warps and groups a lane for rows of d: the weight gradients take 16 registers per group, so 4
-// groups at most.
+// The weight gradients take 16 registers per group of a lane: 2 groups, on as many warps as the row
+// needs up to 8 (with 4 groups on half the warps 94 us instead of 82 us for 16,384 rows of 4,096,
+// 50 us instead of 45 us at 2,048), then 3 and 4 groups, so that two rows are worked on at a time
+// (16 warps of 2 groups, one row at a time: 181 us instead of 103 us for 16,384 rows of 5,120). One
+// group needs few registers: 1,024 threads (262,144 rows of 256: 90 us, with 512 123 us).
 template <class X, class Dy, class Dx, int NV, int WG, bool kMean>
 cudaError_t bwd_rows(const X& x, const Dy& dy, const Dx& dx, const BwdArgs& a, int* parts, int sms,
                      cudaStream_t st) {

@@ -395,6 +395,8 @@ __global__ void __launch_bounds__(256) k_stats_f32(const float* __restrict__ H,
 }
 
 // ------------------------------------------------------------------ launches
+// List lengths compiled: the upkeep grows with K (48 positions over V = 151,936: 103 us without
+// alternatives, 116 us at K = 8, 126 us at K = 32), so one length for all would cost short lists.
 int stats_list_len(int n_top) { return n_top == 0 ? 0 : n_top == 1 ? 1 : n_top <= 8 ? 8 : 32; }
 
 int stats_tiles(bool bf16, int V) {
@@ -404,7 +406,9 @@ int stats_tiles(bool bf16, int V) {
 
 namespace {
 
-// Up to this many positions a block joins each one's tiles, above it a warp.
+// Up to this many positions a block joins each one's tiles, above it a warp: 300 positions over
+// V = 32,000 take 64.5 us in all with blocks and 66.8 us with warps, 1,000 take 114 us with either,
+// 8,000 take 584 us and 550 us.
 constexpr int kBlockJoin = 1024;
 
 template <int K>
