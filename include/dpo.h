@@ -490,8 +490,9 @@ typedef struct {
 dpo_status dpo_norm_workspace_size(int32_t rows, int32_t d, size_t* bytes);
 
 /* The gradients of dpo_norm_forward at x, or, with norm->from, at the values a checkpoint
- * holds. eps and bias are not read. Buffers that overlap otherwise than named above are
- * refused (DPO_ERR_INVALID_ARG). ws: device workspace, 256-byte aligned. */
+ * holds. eps and bias are not read. Rows and checkpoints that overlap otherwise than named
+ * above are refused (DPO_ERR_INVALID_ARG); other buffers must not overlap any written one.
+ * ws: device workspace, 256-byte aligned, for one call at a time. */
 dpo_status dpo_norm_backward(const dpo_norm* norm, const dpo_norm_grads* grads, void* ws,
                              size_t ws_bytes, void* stream);
 
