@@ -160,7 +160,9 @@ __global__ void __launch_bounds__(kThreads) k_norm_bwd_rows(X x, Dy dy, Dx dx, B
   fetch(row, ring);
   fetch(row + step, ring + kSlot);
   // the next row's statistics and scales are asked for while this one is worked on
-  auto stat = [&](const float* p, long long r) { return p != nullptr && r < a.rows ? __ldg(p + r) : 0.f; };
+  auto stat = [&](const float* p, long long r) {
+    return p != nullptr && r < a.rows ? __ldg(p + r) : 0.f;
+  };
   float mu = kMean ? stat(a.mean, row) : 0.f, rs = stat(a.rstd, row);
   typename X::Side side[NV];
   auto sides = [&](long long r) {

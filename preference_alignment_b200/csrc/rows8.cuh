@@ -20,7 +20,9 @@ constexpr int kQBlock = 32;                     // values that share a scale (DP
 
 __host__ __device__ constexpr int q_blocks(int d) { return (d + kQBlock - 1) / kQBlock; }
 // The block of a column (never negative: a shift).
-__host__ __device__ constexpr int q_block_of(int col) { return static_cast<int>(static_cast<unsigned>(col) / kQBlock); }
+__host__ __device__ constexpr int q_block_of(int col) {
+  return static_cast<int>(static_cast<unsigned>(col) / kQBlock);
+}
 
 // ------------------------------------------------------------------ asynchronous copies
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {

@@ -418,7 +418,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
 #pragma unroll
         for (int j = 1; j < kList; ++j) {
           const bool keep = val[j] > kFloor && val[j] >= low;
-          if (open) l[j - 1] = keep ? make_float2(val[j], __int_as_float(id[j])) : make_float2(kFloor, 0.f);
+          if (open)
+            l[j - 1] = keep ? make_float2(val[j], __int_as_float(id[j])) : make_float2(kFloor, 0.f);
           if (j % (kBatch > 0 ? kBatch : 1) == 0) open = keep;
         }
       }

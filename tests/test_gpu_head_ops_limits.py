@@ -13,6 +13,7 @@ from oracle import head_ops_oracle as HO
 from preference_alignment_b200 import libdpo
 from preference_alignment_b200 import workloads as WL
 
+import test_gpu_norm
 from dpo_harness import DeviceWorkload, np64, to_device
 
 pytestmark = pytest.mark.gpu
@@ -184,3 +185,26 @@ def test_optional_operands(d, with_weight, with_bias, dtype, wdtype):
                             WL.widen(w, wdtype) if with_weight else None)
     for got, g, tol in zip((dx, dw, db), want, (half, F32, F32)):
         assert np.abs(np64(got) - g).max() <= tol * np.abs(g).max()
+
+
+# Every group of warps works on several rows, at each length class of the backward.
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("dtype,dy_dtype", [("bf16", "f32"), ("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,d", [(5000, 128), (9700, 136), (9700, 256), (1300, 2048), (900, 4104), (1000, 5128),
+                                    (900, 6144), (900, 6152), (700, 8192)])
+def test_backward_many_rows(rows, d, dtype, dy_dtype, kind):
+    test_gpu_norm.test_backward(rows, d, dtype, dy_dtype, kind)
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("rows,d", [(9700, 200), (1000, 5128), (700, 8192)])
+def test_norm_and_checkpoint_many_rows(rows, d, kind):
+    test_gpu_norm.test_norm_saves_and_reads_a_checkpoint(rows, d, "bf16", kind)
+
+
+# Warps that take 1,024 values of a row or more, and short rows in one line.
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [(3000, 504), (1111, 512), (5000, 520), (5000, 1032), (2500, 4104), (5000, 2056),
+                                    (1700, 8200), (2, 32), (1025, 8), (4097, 24)])
+def test_checkpoint_many_rows(rows, d, dtype):
+    test_gpu_norm.test_checkpoint_holds_the_oracles_codes(rows, d, dtype)
