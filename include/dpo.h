@@ -184,7 +184,9 @@ dpo_status dpo_loss_ex(int32_t B, int32_t layout, const float* pol, const float*
                        void* stream);
 
 /* Backward of sum_r row_coef[r] * seq_logp[r] (step 5) to H and W.
- *   lse_state   device [Nc] fp32 from dpo_seq_logprobs(want_grad=1) on the same batch
+ *   lse_state   device [Nc] fp32 from dpo_seq_logprobs(want_grad=1) or dpo_token_stats on the
+ *               same batch, H and W included: softmax(z) is formed as exp(z - lse), so with
+ *               another H's lse_state the probabilities no longer sum to 1
  *   row_coef    device [R] fp32, d(objective)/d seq_logp[r] (dpo_loss writes it)
  *   dH          device [R, L, d] fp32, 16-byte aligned, out: fully written; 0 at
  *               unscored positions
@@ -359,9 +361,9 @@ dpo_status dpo_logits_mean(const dpo_batch* batch, int32_t layout, float* means,
  *   top     = the n_top largest z: their ids and log-probs z - lse, in falling order,
  *             equal logits by rising id
  * (dpo_seq_logprobs' forward with what monitoring and serving ask for beside the target's
- * log-prob.) The gradient of the log-probs is dpo_backward on the lse_state written here;
- * the entropy and the alternatives are metrics and have none. The same inputs give the same
- * bits on every run.
+ * log-prob.) The gradient of the log-probs is dpo_backward on the lse_state written here and
+ * the same H and W; the entropy and the alternatives are metrics and have none. The same
+ * inputs give the same bits on every run.
  *   Any pointer may be NULL: that value is not wanted. top_ids and top_logp are [n, n_top],
  *   n_top in 0 .. DPO_MAX_TOP; with n_top > 0 both are required.
  *   A row with fewer than n_top logits above -1e30 (a small vocabulary, infinities) ends in
@@ -467,8 +469,11 @@ typedef struct {
  *   mean   device [rows] fp32 or NULL (NULL for rms)
  *   rstd   device [rows] fp32 or NULL
  *   save   also hold x in this checkpoint, or NULL; not together with `from`
- * With `from` the checkpoint's values take x's place, the statistics too: it forms H again
- * for the backward without the forward's x. */
+ * With `from` the checkpoint's values take x's place, the statistics too, so H can be formed
+ * without x. That H is not the one formed from x (each value is off by the codes' rounding),
+ * and dpo_backward's lse_state belongs to one H: a step whose backward forms H again either
+ * forms it from the checkpoint for its forward too (the same bits both times), or takes
+ * dpo_token_stats or dpo_seq_logprobs of the H formed again. */
 dpo_status dpo_norm_forward(const dpo_norm* norm, void* y, int64_t y_stride, float* mean,
                             float* rstd, const dpo_checkpoint* save, void* stream);
 
@@ -489,9 +494,11 @@ typedef struct {
 /* Workspace bytes of dpo_norm_backward. Pure host function. */
 dpo_status dpo_norm_workspace_size(int32_t rows, int32_t d, size_t* bytes);
 
-/* The gradients of dpo_norm_forward at x, or, with norm->from, at the values a checkpoint
- * holds. eps and bias are not read. Rows and checkpoints that overlap otherwise than named
- * above are refused (DPO_ERR_INVALID_ARG); other buffers must not overlap any written one.
+/* The gradients of dpo_norm_forward: the formulas above with the given mean and rstd, at x or,
+ * with norm->from, at the values a checkpoint holds. With the statistics of x that a forward
+ * with `save` wrote, xh = (held value - mean of x) * rstd of x: the forward's own scaling, of
+ * values off by the codes' rounding. eps and bias are not read. Rows and checkpoints that
+ * overlap otherwise than named above are refused (DPO_ERR_INVALID_ARG); other buffers must not overlap any written one.
  * ws: device workspace, 256-byte aligned, for one call at a time. */
 dpo_status dpo_norm_backward(const dpo_norm* norm, const dpo_norm_grads* grads, void* ws,
                              size_t ws_bytes, void* stream);

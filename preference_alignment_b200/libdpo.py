@@ -635,8 +635,8 @@ def token_stats_size(batch: BatchArgs, n_top: int):
 def token_stats(batch: BatchArgs, n_top: int, ws, logp=None, entropy=None, lse_state=None,
                 seq_logp=None, top_ids=None, top_logp=None, ws_bytes=None, stream=None):
     """dpo_token_stats: per scored position (row order) the target's log-prob, the entropy, the
-    log-sum-exp that backward() reads and the n_top largest logits' ids and log-probs; per row
-    the sum of the log-probs. Outputs left out are not written."""
+    log-sum-exp that backward() reads with the same H and W, and the n_top largest logits' ids and
+    log-probs; per row the sum of the log-probs. Outputs left out are not written."""
     dev = _device()
     out = _stats_out(batch.n_scored, n_top, logp, entropy, lse_state, top_ids, top_logp, dev)
     w, nbytes = _work(ws, ws_bytes, dev)
@@ -750,7 +750,8 @@ def norm_forward(x, y, weight=None, bias=None, kind="layer", eps=1e-5, mean=None
                  save: Optional[Checkpoint] = None, stream=None):
     """dpo_norm_forward: y = norm(x) by rows, kind "layer" or "rms"; mean and rstd (f32 [rows])
     are what norm_backward reads; save also holds x in 8 bits. x may be a Checkpoint: the norm
-    of the values it holds."""
+    of the values it holds (not the H that was formed from x itself: backward() takes an lse_state
+    of the H it is given)."""
     dev = _device()
     ykind = _kind_of(y)
     n, rows, d = _norm(x, ykind, weight, bias, kind, eps, dev)
