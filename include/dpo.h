@@ -365,7 +365,8 @@ dpo_status dpo_logits_mean(const dpo_batch* batch, int32_t layout, float* means,
  * the same H and W; the entropy and the alternatives are metrics and have none. The same
  * inputs give the same bits on every run.
  *   Any pointer may be NULL: that value is not wanted. top_ids and top_logp are [n, n_top],
- *   n_top in 0 .. DPO_MAX_TOP; with n_top > 0 both are required.
+ *   n_top in 0 .. DPO_MAX_TOP; with n_top > 0 both are required (n > 0: without positions
+ *   nothing is written and no output is needed).
  *   A row with fewer than n_top logits above -1e30 (a small vocabulary, infinities) ends in
  *   id -1, log-prob -inf. A NaN logit makes the row's lse, logp and entropy NaN and is no
  *   alternative. A token outside [0, V) is a bad target: logp 0, the status word as for

@@ -541,9 +541,11 @@ StatsPlan stats_fit(size_t prefix, long long n_lp, long long n, int V, bool bf16
   return s;
 }
 
-dpo_status stats_out_ok(const dpo_token_stats_out* o) {
+// The outputs of n positions (none: nothing is written, so no pointer is needed).
+dpo_status stats_out_ok(const dpo_token_stats_out* o, long long n) {
   if (o == nullptr || o->n_top < 0 || o->n_top > DPO_MAX_TOP) return DPO_ERR_INVALID_ARG;
-  if (o->n_top > 0 && (o->top_ids == nullptr || o->top_logp == nullptr)) return DPO_ERR_INVALID_ARG;
+  if (n > 0 && o->n_top > 0 && (o->top_ids == nullptr || o->top_logp == nullptr))
+    return DPO_ERR_INVALID_ARG;
   return DPO_OK;
 }
 
@@ -757,7 +759,7 @@ dpo_status dpo_token_stats(const dpo_batch* batch, const dpo_token_stats_out* ou
   Plan p;
   dpo_status s = make_plan(batch, &p);
   if (s != DPO_OK) return s;
-  if ((s = stats_out_ok(out)) != DPO_OK) return s;
+  if ((s = stats_out_ok(out, p.Nc)) != DPO_OK) return s;
   const bool bf16 = p.dtype == DPO_BF16;
   if (!ws_ok(ws, ws_bytes, 1)) return DPO_ERR_WORKSPACE;
   const StatsPlan sp = stats_fit(p.prefix, p.Nc, p.Nc, p.V, bf16, out->n_top, ws_bytes);
@@ -796,7 +798,7 @@ dpo_status dpo_token_stats_rows(const dpo_token_rows* rows, const dpo_token_stat
   NvtxRange nvtx_range("dpo_token_stats_rows");
   dpo_status s = token_rows_ok(rows, false);
   if (s != DPO_OK) return s;
-  if ((s = stats_out_ok(out)) != DPO_OK) return s;
+  if ((s = stats_out_ok(out, rows->n)) != DPO_OK) return s;
   if (out->logp != nullptr && rows->tokens == nullptr && rows->n > 0) return DPO_ERR_INVALID_ARG;
   if (rows->n == 0) return DPO_OK;
   const bool bf16 = rows->dtype == DPO_BF16;
