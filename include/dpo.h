@@ -383,7 +383,7 @@ typedef struct {
 
 /* Workspace bytes of dpo_token_stats for this batch and n_top; a workspace of at least
  * *min_bytes (may be NULL) makes it run in several chunks of positions, with the same
- * results within rounding. Pure host function. */
+ * bits. Pure host function. */
 dpo_status dpo_token_stats_size(const dpo_batch* batch, int32_t n_top, size_t* bytes,
                                 size_t* min_bytes);
 

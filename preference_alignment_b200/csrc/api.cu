@@ -570,7 +570,8 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
                        o.lse_state ? o.lse_state + i0 : nullptr,
                        o.n_top ? o.top_logp + i0 * o.n_top : nullptr,
                        o.n_top ? o.top_ids + i0 * o.n_top : nullptr, o.n_top};
-    // by the call's n: a chunk never changes the route
+    // The route and the join go by the call's n, so that a position's bits do not depend on the
+    // chunk it falls into, nor on the workspace.
     if (bf16 && n <= kStreamMax) {
       const int ctas = stats_stream_ctas(V, di.sms);
       CUtensorMap mW, mH;
@@ -596,7 +597,7 @@ dpo_status stats_core(const StatsPlan& s, uint8_t* w, int* sync, long long n, in
           cudaSuccess)
         return DPO_ERR_CUDA;
     }
-    if (launch_stats_finish(b, bf16, stats_tiles(bf16, V), m, V, yc, out, ctl, st) != cudaSuccess)
+    if (launch_stats_finish(b, bf16, stats_tiles(bf16, V), m, n, V, yc, out, ctl, st) != cudaSuccess)
       return DPO_ERR_CUDA;
   }
   return DPO_OK;

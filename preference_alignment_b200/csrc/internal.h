@@ -181,9 +181,10 @@ int stats_stream_rows(int V, int ctas);   // vocabulary rows per tile
 cudaError_t launch_stats_stream(const CUtensorMap& mapW, const CUtensorMap& mapH,
                                 const StatsBuf& b, const StatsOut& out, int n, int V, int d,
                                 const int* y, int ctas, const DevCtl& ctl, cudaStream_t st);
-// Joins the S tiles of the GEMM's or the SIMT route's partials (thresholds: the GEMM's).
-cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int n, int V,
-                                const int* y, const StatsOut& out, const DevCtl& ctl,
+// Joins the S tiles of the GEMM's or the SIMT route's partials (thresholds: the GEMM's) for n
+// positions, a chunk of the call's n_call.
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int n, long long n_call,
+                                int V, const int* y, const StatsOut& out, const DevCtl& ctl,
                                 cudaStream_t st);
 
 // 8-bit activation checkpoints (checkpoint.cu) and the norm before the head (norm.cu).

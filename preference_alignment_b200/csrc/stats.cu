@@ -406,7 +406,7 @@ int stats_tiles(bool bf16, int V) {
 
 namespace {
 
-// Up to this many positions a block joins each one's tiles, above it a warp: 300 positions over
+// Calls of up to this many positions join each one's tiles by a block, larger ones by a warp: 300 positions over
 // V = 32,000 take 64.5 us in all with blocks and 66.8 us with warps, 1,000 take 114 us with either,
 // 8,000 take 584 us and 550 us.
 constexpr int kBlockJoin = 1024;
@@ -426,10 +426,10 @@ cudaError_t stats_bf16(const CUtensorMap& mapA, const CUtensorMap& mapB, const S
 }
 
 template <int K>
-cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, int S, int V, const int* y,
-                         const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
+cudaError_t stats_finish(const StatsBuf& b, bool with_tau, int n, long long n_call, int S, int V,
+                         const int* y, const StatsOut& out, const DevCtl& ctl, cudaStream_t st) {
   const uint32_t* tau = with_tau ? b.tau : nullptr;
-  if (n <= kBlockJoin && S <= kJoinSets)
+  if (n_call <= kBlockJoin && S <= kJoinSets)
     return launch_join<K>(TileSets<K>{b.part, b.tsum, b.list, tau, S, b.ldp}, y, b.zy, n, V, out, ctl,
                           st);
   return launch_after(k_stats_finish<K>, dim3((n + 7) / 8), 256, st, b.part, b.tsum, b.list, tau, b.zy,
@@ -464,10 +464,11 @@ cudaError_t launch_stats_f32(const float* H, const int* at, long long h_stride, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int n, int V,
-                                const int* y, const StatsOut& out, const DevCtl& ctl,
+cudaError_t launch_stats_finish(const StatsBuf& b, bool thresholds, int S, int n, long long n_call,
+                                int V, const int* y, const StatsOut& out, const DevCtl& ctl,
                                 cudaStream_t st) {
-  return DPO_BY_LIST(stats_list_len(out.n_top), stats_finish)(b, thresholds, n, S, V, y, out, ctl, st);
+  return DPO_BY_LIST(stats_list_len(out.n_top), stats_finish)(b, thresholds, n, n_call, S, V, y, out,
+                                                              ctl, st);
 }
 
 }  // namespace dpo
