@@ -381,9 +381,10 @@ typedef struct {
   float* top_logp;    /* device [n, n_top]                                               */
 } dpo_token_stats_out;
 
-/* Workspace bytes of dpo_token_stats for this batch and n_top; a workspace of at least
- * *min_bytes (may be NULL) makes it run in several chunks of positions, with the same
- * bits. Pure host function. */
+/* Workspace bytes of dpo_token_stats for this batch and n_top: the batch's packed rows and
+ * about 1 GB at most of partial results (more only where the smallest chunk, 256 positions or
+ * 32 in fp32, needs it). A workspace of at least *min_bytes (may be NULL) makes it run in
+ * several, or more, chunks of positions, with the same bits. Pure host function. */
 dpo_status dpo_token_stats_size(const dpo_batch* batch, int32_t n_top, size_t* bytes,
                                 size_t* min_bytes);
 

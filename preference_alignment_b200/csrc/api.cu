@@ -479,9 +479,14 @@ dpo_status backward_core(const Plan& p, const dpo_batch* batch, const float* lse
 }
 
 // ---------------------------------------------------------------- token statistics
-// Positions a launch takes at most: the tiles' partials and lists of a chunk stay within a few
-// hundred MB, and 8,192 positions are enough tiles to fill the GPU's waves.
+// Positions a launch takes at most: 8,192 are enough tiles to fill the GPU's waves, and the tiles'
+// partials and lists of a chunk stay within 1 GB, but for the least a launch takes (12 + 8 K bytes
+// per tile and position: 0.31 GB for 8,192 positions at V = 128,256 with K = 8; without the second
+// bound 1.3 GB at V = 151,936 with K = 32 and, with the fp32 route's tiles of 32 rows, 8.8 GB at
+// V = 128,256). Cut at 512 MB, 1,000 fp32 positions at d = 64, V = 128,256, K = 32 take 2.32 ms, at
+// 1 GB 2.24 ms, uncut (1.1 GB) 2.12 ms; bf16 calls of 9,000 positions take the same time cut or not.
 constexpr int kStatsChunk = 8192;
+constexpr size_t kStatsChunkBytes = 1u << 30;
 
 struct StatsPlan {
   int chunk = 0;                       // positions per launch
@@ -522,17 +527,26 @@ StatsPlan stats_layout(size_t prefix, long long n_lp, long long n, int V, bool b
   return s;
 }
 
-int stats_chunk_max(long long n) { return static_cast<int>(std::min<long long>(n, kStatsChunk)); }
-// The smallest chunk: one tile of token rows of a CTA pair, or of the SIMT route's.
+// Chunks are whole tiles of token rows of a CTA pair, or of the SIMT route's, but for a call's last.
+constexpr int stats_step(bool bf16) { return bf16 ? 256 : 32; }
+// The smallest chunk.
 int stats_chunk_min(long long n, bool bf16) {
-  return static_cast<int>(std::min<long long>(n, bf16 ? 256 : 32));
+  return static_cast<int>(std::min<long long>(n, stats_step(bf16)));
+}
+// The largest.
+int stats_chunk_max(long long n, int V, bool bf16, int n_top) {
+  const int step = stats_step(bf16);
+  const size_t entry = sizeof(float2) + sizeof(float) + sizeof(float2) * stats_list_len(n_top);
+  const size_t fit = kStatsChunkBytes / (entry * stats_tiles(bf16, V)) / step * step;
+  const long long most = std::max<long long>(step, std::min<long long>(fit, kStatsChunk));
+  return static_cast<int>(std::min(n, most));
 }
 
 // The largest chunk the workspace takes (total > ws_bytes: not even the smallest fits).
 StatsPlan stats_fit(size_t prefix, long long n_lp, long long n, int V, bool bf16, int n_top,
                     size_t ws_bytes) {
-  const int step = bf16 ? 256 : 32;
-  int chunk = stats_chunk_max(n);
+  const int step = stats_step(bf16);
+  int chunk = stats_chunk_max(n, V, bf16, n_top);
   StatsPlan s = stats_layout(prefix, n_lp, n, V, bf16, n_top, chunk);
   while (s.total > ws_bytes && chunk > stats_chunk_min(n, bf16)) {
     chunk = (chunk - 1) / step * step;
@@ -748,7 +762,9 @@ dpo_status dpo_token_stats_size(const dpo_batch* batch, int32_t n_top, size_t* b
   if (s != DPO_OK) return s;
   if (n_top < 0 || n_top > DPO_MAX_TOP) return DPO_ERR_INVALID_ARG;
   const bool bf16 = p.dtype == DPO_BF16;
-  if (bytes) *bytes = stats_layout(p.prefix, p.Nc, p.Nc, p.V, bf16, n_top, stats_chunk_max(p.Nc)).total;
+  if (bytes)
+    *bytes = stats_layout(p.prefix, p.Nc, p.Nc, p.V, bf16, n_top,
+                          stats_chunk_max(p.Nc, p.V, bf16, n_top)).total;
   if (min_bytes)
     *min_bytes = stats_layout(p.prefix, p.Nc, p.Nc, p.V, bf16, n_top, stats_chunk_min(p.Nc, bf16)).total;
   return DPO_OK;
@@ -788,7 +804,8 @@ dpo_status dpo_token_stats_rows_size(const dpo_token_rows* rows, int32_t n_top, 
   const bool bf16 = rows->dtype == DPO_BF16;
   const long long n = rows->n;
   if (bytes)
-    *bytes = stats_layout(kRowsPrefix, 0, n, rows->V, bf16, n_top, stats_chunk_max(n)).total;
+    *bytes = stats_layout(kRowsPrefix, 0, n, rows->V, bf16, n_top,
+                          stats_chunk_max(n, rows->V, bf16, n_top)).total;
   if (min_bytes)
     *min_bytes = stats_layout(kRowsPrefix, 0, n, rows->V, bf16, n_top, stats_chunk_min(n, bf16)).total;
   return DPO_OK;

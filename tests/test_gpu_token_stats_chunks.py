@@ -71,3 +71,24 @@ def test_both_gemm_kernels_give_the_same_bits(n, d, V):
     for g in got[1:]:
         for k, v in got[0].items():
             assert np.array_equal(v, g[k]), k
+
+
+def test_default_workspace_cut_by_its_bytes():
+    """2,100 fp32 positions with 32 alternatives over 80,000 rows take more than the 1 GB that a
+    chunk may: two launches, the ids exact on a grid."""
+    import torch
+    n, d, V, n_top = 2100, 8, 80000, 32
+    rng = np.random.default_rng(9)
+    hs = (np.rint(rng.normal(size=(n, d)) * 8) / 8).astype(np.float32)
+    Ws = (np.rint(rng.normal(size=(V, d)) * 64) / 64).astype(np.float32)
+    tokens = rng.integers(0, V, n).astype(np.int32)
+    size = libdpo.token_stats_rows_size(n, d, V, n_top, "f32")[0]
+    assert size < (V // 32) * n * 268                  # what one launch of all would take
+    got = _run(torch.from_numpy(hs).cuda(), torch.from_numpy(Ws).cuda(),
+               torch.from_numpy(tokens).cuda(), n_top, "f32", size)
+    for i in (0, 1400, 1980):                          # the oracle in parts: both launches, the last rows
+        s = slice(i, i + 120)
+        o = HO.token_stats(hs[s], Ws, tokens[s], n_top)
+        assert np.array_equal(got["top_ids"][s], o["top_ids"])
+        # exact logits; sums as above
+        assert np.all(np.abs(got["lse_state"][s] - o["lse"]) <= 2.0 ** -15 + 2.0 ** -23 * np.abs(o["lse"]))
