@@ -161,7 +161,7 @@ Grid grid_of(int rows, int d) {
   int span = 4 * kStep;
   while (span > kStep && static_cast<long long>(rows) * ((d + span - 1) / span) < kManyWarps)
     span -= kStep;
-  return {static_cast<long long>((d + span - 1) / span) * ((rows + kWarps - 1) / kWarps), span};
+  return {static_cast<long long>((d + span - 1) / span) * ((static_cast<long long>(rows) + kWarps - 1) / kWarps), span};
 }
 
 template <class Src>

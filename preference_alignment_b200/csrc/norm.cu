@@ -224,13 +224,13 @@ cudaError_t fwd_rows(const Src& x, const Out& y, const FwdArgs& a, int sms, cuda
   auto kern = k_norm_fwd_rows<Src, Out, NV, WG, kThreads>;
   const size_t vec = 2 * sizeof(float) * static_cast<size_t>(a.d);
   const size_t slot = static_cast<size_t>(NV) * WG * 32 * Src::kSlot;
-  const int per_sm = (a.rows + sms - 1) / sms;
+  const int per_sm = blocks_of(a.rows, sms);
   int groups = std::min<int>(kThreads / (WG * 32), (kSmemBytes - vec) / slot);
   groups = std::max(1, std::min(groups, per_sm));
   const size_t smem = vec + groups * slot;
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(sms, (a.rows + groups - 1) / groups);
+  const int grid = std::min(sms, blocks_of(a.rows, groups));
   kern<<<grid, groups * WG * 32, smem, st>>>(x, y, a);
   return cudaGetLastError();
 }

@@ -94,6 +94,11 @@ __device__ __forceinline__ float block_total(float x, float* buf) {
 constexpr int kWideThreads = 512;
 constexpr int kSmemBytes = 226 * 1024;    // dynamic shared memory a block may ask for
 
+// Blocks of `each` rows (rows up to 2^31 - 1: the sum takes 64 bits).
+inline int blocks_of(int rows, int each) {
+  return static_cast<int>((static_cast<long long>(rows) + each - 1) / each);
+}
+
 inline int short_lanes(int d) {
   int g = 1;
   while (g * 8 < d) g *= 2;

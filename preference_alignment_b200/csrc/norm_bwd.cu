@@ -428,13 +428,13 @@ cudaError_t bwd_rows(const X& x, const Dy& dy, const Dx& dx, const BwdArgs& a, i
   auto kern = k_norm_bwd_rows<X, Dy, Dx, NV, WG, kThreads, kMean>;
   const size_t vec = sizeof(float) * static_cast<size_t>(a.d);
   const size_t slots = static_cast<size_t>(kSlots) * NV * WG * 32 * (X::kSlot + Dy::kSlot);
-  const int per_sm = (a.rows + sms - 1) / sms;
+  const int per_sm = blocks_of(a.rows, sms);
   int groups = std::min<int>(kThreads / (WG * 32), (kSmemBytes - vec) / slots);
   groups = std::max(1, std::min(groups, per_sm));
   const size_t smem = vec + groups * std::max(slots, vec);   // the gradients meet in the slots
   const cudaError_t e = allow_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  *parts = std::min(std::min(sms, norm_parts(a.d)), (a.rows + groups - 1) / groups);
+  *parts = std::min(std::min(sms, norm_parts(a.d)), blocks_of(a.rows, groups));
   kern<<<*parts, groups * WG * 32, smem, st>>>(x, dy, dx, a);
   return cudaGetLastError();
 }
@@ -481,7 +481,7 @@ cudaError_t norm_bwd(const X& x, const Dy& dy, const Dx& dx, BwdArgs a, float* w
     e = cudaGetLastError();
   } else if (a.d <= kMaxShort) {
     const int rows_at_once = kShortThreads / short_lanes(a.d);
-    parts = std::min(std::min(4 * sms, norm_parts(a.d)), (a.rows + rows_at_once - 1) / rows_at_once);
+    parts = std::min(std::min(4 * sms, norm_parts(a.d)), blocks_of(a.rows, rows_at_once));
     e = bwd_short(x, dy, dx, a, parts, st);
   } else if (a.mean != nullptr) {
     e = bwd_by_length<X, Dy, Dx, true>(x, dy, dx, a, &parts, sms, st);
