@@ -530,6 +530,17 @@ def _buf(x, kind, n, what, dev):
     return x.data_ptr()
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _c32(n, what):
+    """n as the C ABI's 32-bit integer, which would silently take the low bits of a larger one."""
+    n = int(n)
+    if n > _MOST or n < -_MOST - 1:
+        raise ValueError(f"{what}: {n} does not fit 32 bits")
+    return n
+
+
 def _row_view(x, what, dev):
     """(address, rows, d, stride) of a tensor of rows: 2-D with dense rows (any row stride), or
     contiguous of any shape with its last dimension the row."""
@@ -540,11 +551,13 @@ def _row_view(x, what, dev):
         rows, d = shape
         stride, inner = x.stride()
         if inner == 1 and d > 0:
+            if rows > _MOST or d > _MOST:
+                _c32(max(rows, d), what)
             return x.data_ptr(), rows, d, (stride if rows > 1 else d)
     if len(shape) == 0 or shape[-1] < 1 or not x.is_contiguous():
         raise ValueError(f"{what}: tensor of shape {tuple(shape)} has no dense rows")
     d = shape[-1]
-    return x.data_ptr(), x.numel() // d, d, d
+    return x.data_ptr(), _c32(x.numel() // d, what), _c32(d, what), d
 
 
 def _work(ws, ws_bytes, dev):
@@ -616,7 +629,7 @@ _NORM_BWD = [_normp, _gradsp, _vp, _sz, _vp]
 
 
 def _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp, dev):
-    n_top = int(n_top)
+    n_top = _c32(n_top, "n_top")
     return TokenStatsOut(_buf(logp, "f32", n, "logp", dev), _buf(entropy, "f32", n, "entropy", dev),
                          _buf(lse_state, "f32", n, "lse_state", dev), n_top,
                          _buf(top_ids, "i32", n * n_top, "top_ids", dev),
@@ -626,7 +639,7 @@ def _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp, dev):
 def token_stats_size(batch: BatchArgs, n_top: int):
     """(bytes, min_bytes) of token_stats' workspace."""
     a, b = _sz(), _sz()
-    _check(_fn("dpo_token_stats_size", _STATS_SIZE)(ctypes.byref(batch.c), int(n_top),
+    _check(_fn("dpo_token_stats_size", _STATS_SIZE)(ctypes.byref(batch.c), _c32(n_top, "n_top"),
                                                     ctypes.byref(a), ctypes.byref(b)),
            "dpo_token_stats_size")
     return a.value, b.value
@@ -648,9 +661,9 @@ def token_stats(batch: BatchArgs, n_top: int, ws, logp=None, entropy=None, lse_s
 def token_stats_rows_size(n: int, d: int, V: int, n_top: int, dtype="bf16"):
     """(bytes, min_bytes) of token_stats_rows' workspace."""
     a, b = _sz(), _sz()
-    rows = TokenRows(int(n), int(d), int(V), DTYPES[dtype] if isinstance(dtype, str) else int(dtype),
-                     None, int(d), None, None)
-    _check(_fn("dpo_token_stats_rows_size", _ROWS_SIZE)(ctypes.byref(rows), int(n_top),
+    rows = TokenRows(_c32(n, "n"), _c32(d, "d"), _c32(V, "V"),
+                     DTYPES[dtype] if isinstance(dtype, str) else int(dtype), None, int(d), None, None)
+    _check(_fn("dpo_token_stats_rows_size", _ROWS_SIZE)(ctypes.byref(rows), _c32(n_top, "n_top"),
                                                         ctypes.byref(a), ctypes.byref(b)),
            "dpo_token_stats_rows_size")
     return a.value, b.value
@@ -665,7 +678,7 @@ def token_stats_rows(H, W, tokens, n_top: int, ws, logp=None, entropy=None, lse_
     if len(W.shape) != 2 or W.shape[1] != d:
         raise ValueError(f"W of shape {tuple(W.shape)} does not fit rows of {d}")
     kind = _kind_of(H)
-    rows = TokenRows(n, d, W.shape[0], DTYPES[kind], h, stride, _buf(W, kind, 0, "W", dev),
+    rows = TokenRows(n, d, _c32(W.shape[0], "W"), DTYPES[kind], h, stride, _buf(W, kind, 0, "W", dev),
                      _buf(tokens, "i32", n, "tokens", dev))
     out = _stats_out(n, n_top, logp, entropy, lse_state, top_ids, top_logp, dev)
     w, nbytes = _work(ws, ws_bytes, dev)
@@ -728,7 +741,7 @@ def _norm(x, kind_out, weight, bias, kind, eps, dev):
     """(NormC, rows, d) of a norm of x, a tensor of rows or a Checkpoint (then kind_out is the
     other side's element type)."""
     if isinstance(x, Checkpoint):
-        p, rows, d, stride = None, x.rows, x.d, 0
+        p, rows, d, stride = None, _c32(x.rows, "rows"), _c32(x.d, "d"), 0
         held = ctypes.pointer(x._c(dev))
     else:
         p, rows, d, stride = _row_view(x, "x", dev)
@@ -772,7 +785,7 @@ def norm_forward(x, y, weight=None, bias=None, kind="layer", eps=1e-5, mean=None
 def norm_workspace_size(rows: int, d: int) -> int:
     """Workspace bytes of norm_backward."""
     b = _sz()
-    _check(_fn("dpo_norm_workspace_size", _NORM_WS)(int(rows), int(d), ctypes.byref(b)),
+    _check(_fn("dpo_norm_workspace_size", _NORM_WS)(_c32(rows, "rows"), _c32(d, "d"), ctypes.byref(b)),
            "dpo_norm_workspace_size")
     return b.value
 
