@@ -103,7 +103,9 @@ def backward_exchange(batch, lse_state, row_coef, dH, dW, ws, n_buckets=8, max_s
     then dW block by block with each block's all-reduce started as soon as it is
     formed, then dH while the last all-reduce runs, then (norm: a FinalNorm) the final
     norm's backward on that dH, whose weight gradients are all-reduced as well. max_sms > 0
-    leaves the other SMs free for the collective's kernels. Everything is enqueued on
+    leaves the other SMs free for the collective's kernels while any are pending: dW and dH
+    keep to it, and the norm's backward, which takes every SM, starts when dW's all-reduces
+    are done (without a budget it runs beside them). Everything is enqueued on
     torch's current stream, the stream the collectives order against. Returns the pending
     works (finish() them). ops: the calls to make (default: the library)."""
     import torch.distributed as dist
@@ -119,6 +121,8 @@ def backward_exchange(batch, lse_state, row_coef, dH, dW, ws, n_buckets=8, max_s
     if dH is not None:
         ops.backward_dh(batch, dH, ws, max_sms=max_sms)
     if norm is not None:
+        if max_sms > 0:
+            finish(works)
         norm.backward(dH, ops)
         works += [dist.all_reduce(g, group=group, async_op=True) for g in norm.reduced()]
     return works
