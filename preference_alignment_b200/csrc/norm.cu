@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kWideThreads) k_norm_fwd_wide(Src x, Out y, Fw
   }
 }
 
+constexpr int kMaxShortFwd = 256;       // longest row of the short form
 constexpr int kMaxFwd = 16384;          // longest row of the groups: 8 warps of 8 groups a lane
 
 // As many warps as registers allow (about 8 NV + 60 a thread), in one block per SM so that the
@@ -235,18 +236,22 @@ cudaError_t fwd_rows(const Src& x, const Out& y, const FwdArgs& a, int sms, cuda
   return cudaGetLastError();
 }
 
-template <class Src, class Out, int WG>
+// Rows of more than kMin values. (2 and 8 warps take rows that 1 and 4 cannot hold: 5 groups a lane at
+// least.)
+template <class Src, class Out, int WG, int kMin>
 cudaError_t fwd_by_length(const Src& x, const Out& y, const FwdArgs& a, int sms, cudaStream_t st) {
   const int nv = (a.d + WG * 256 - 1) / (WG * 256);
-  if (nv <= 2) return fwd_rows<Src, Out, 2, WG>(x, y, a, sms, st);
-  if (nv <= 4) return fwd_rows<Src, Out, 4, WG>(x, y, a, sms, st);
+  if constexpr (kMin < 2 * WG * 256)
+    if (nv <= 2) return fwd_rows<Src, Out, 2, WG>(x, y, a, sms, st);
+  if constexpr (kMin < 4 * WG * 256)
+    if (nv <= 4) return fwd_rows<Src, Out, 4, WG>(x, y, a, sms, st);
   if (nv <= 6) return fwd_rows<Src, Out, 6, WG>(x, y, a, sms, st);
   return fwd_rows<Src, Out, 8, WG>(x, y, a, sms, st);
 }
 
 template <class Src, class Out>
 cudaError_t norm_fwd(const Src& x, const Out& y, const FwdArgs& a, int sms, cudaStream_t st) {
-  if (a.d <= 256) {
+  if (a.d <= kMaxShortFwd) {
     const int g = short_lanes(a.d);
     const int grid = static_cast<int>((static_cast<long long>(a.rows) * g + 255) / 256);
     switch (g) {
@@ -266,10 +271,10 @@ cudaError_t norm_fwd(const Src& x, const Out& y, const FwdArgs& a, int sms, cuda
   // the fewest warps per row that leave a lane 8 groups (a row of 4,096 on one warp of 16 groups a
   // lane: 51 us instead of 47 us for 16,384 rows, on four warps of 4: 47.5 us; at 2,048 one warp 27
   // us, four 31 us); 4 where there are fewer rows than SMs, so that a row's latency is spread
-  if (a.d > 8192) return fwd_by_length<Src, Out, 8>(x, y, a, sms, st);
-  if (a.d > 4096 || a.rows <= sms) return fwd_by_length<Src, Out, 4>(x, y, a, sms, st);
-  if (a.d > 2048) return fwd_by_length<Src, Out, 2>(x, y, a, sms, st);
-  return fwd_by_length<Src, Out, 1>(x, y, a, sms, st);
+  if (a.d > 8192) return fwd_by_length<Src, Out, 8, 8192>(x, y, a, sms, st);
+  if (a.d > 4096 || a.rows <= sms) return fwd_by_length<Src, Out, 4, kMaxShortFwd>(x, y, a, sms, st);
+  if (a.d > 2048) return fwd_by_length<Src, Out, 2, 2048>(x, y, a, sms, st);
+  return fwd_by_length<Src, Out, 1, kMaxShortFwd>(x, y, a, sms, st);
 }
 
 }  // namespace

@@ -454,13 +454,13 @@ cudaError_t bwd_by_length(const X& x, const Dy& dy, const Dx& dx, const BwdArgs&
 template <class X, class Dy, class Dx>
 cudaError_t bwd_short(const X& x, const Dy& dy, const Dx& dx, const BwdArgs& a, int parts,
                       cudaStream_t st) {
+  static_assert(kMaxShort <= 16 * 8, "rows of 16 lanes at most");
   switch (short_lanes(a.d)) {
     case 1: k_norm_bwd_short<X, Dy, Dx, 1><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
     case 2: k_norm_bwd_short<X, Dy, Dx, 2><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
     case 4: k_norm_bwd_short<X, Dy, Dx, 4><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
     case 8: k_norm_bwd_short<X, Dy, Dx, 8><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
-    case 16: k_norm_bwd_short<X, Dy, Dx, 16><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
-    default: k_norm_bwd_short<X, Dy, Dx, 32><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
+    default: k_norm_bwd_short<X, Dy, Dx, 16><<<parts, kShortThreads, 0, st>>>(x, dy, dx, a); break;
   }
   return cudaGetLastError();
 }
