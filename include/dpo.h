@@ -501,7 +501,8 @@ dpo_status dpo_norm_workspace_size(int32_t rows, int32_t d, size_t* bytes);
  * with `save` wrote, xh = (held value - mean of x) * rstd of x: the forward's own scaling, of
  * values off by the codes' rounding. eps and bias are not read. Rows and checkpoints that
  * overlap otherwise than named above are refused (DPO_ERR_INVALID_ARG); other buffers must not overlap any written one.
- * ws: device workspace, 256-byte aligned, for one call at a time. */
+ * ws: device workspace, 256-byte aligned, for one call at a time; asked for in every call, also
+ * when only dx is wanted. */
 dpo_status dpo_norm_backward(const dpo_norm* norm, const dpo_norm_grads* grads, void* ws,
                              size_t ws_bytes, void* stream);
 

@@ -7,7 +7,7 @@
 //   long rows   a warp takes `span` values of one row, 1,024 at a time
 //   short rows  the rows are one line of places, 4 per block of 32 (a row's last block may leave
 //               some empty), and a thread block takes its next kPlaces * kThreads: every lane has
-//               work, at the price of a division per group
+//               work, at the price of two divisions per group (70 % of the copy rate)
 // Pack of 262,144 rows of 256: 44 us in the line, 84 us by rows; of 512: 86 us and 112 us; 100,000
 // rows of 1,000: 64 us and 58 us.
 #include <climits>

@@ -7,8 +7,9 @@
 //              warp per row 73 us; of 256: 113 us and 90 us)
 //   d <= 8192  groups of 1 to 8 warps per row (8,192 rows of 8,192: 95 us; as below 168 us)
 //   above      a block per row that reads it twice, and a column sum that reads it again: the weight
-//              gradients of a row of 16,384 no longer fit the registers and shared memory of an SM
-//              beside two rows (4,096 rows of 16,384: 158 us, half the rate)
+//              gradients of a row of 16,384 no longer fit the registers and shared memory of one SM
+//              beside two rows (4,096 rows of 16,384: 158 us, half the rate). A row split over a
+//              cluster of two would; it is not built.
 #include "chain.cuh"
 #include "norm.cuh"
 

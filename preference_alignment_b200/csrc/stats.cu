@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(256) k_stats_f32(const float* __restrict__ H,
 }
 
 // ------------------------------------------------------------------ launches
-// List lengths compiled: the upkeep grows with K (48 positions over V = 151,936: 103 us without
-// alternatives, 116 us at K = 8, 126 us at K = 32), so one length for all would cost short lists.
+// List lengths compiled: the upkeep grows with K (48 positions over V = 151,936, d = 2,048: 103 us
+// without alternatives, 106, 110 and 121 us at K = 1, 8 and 32; 8,000 over V = 32,000, d = 512, where the
+// upkeep is most of the time: 235, 274, 446 and 1131 us), so one length for all would cost short lists.
 int stats_list_len(int n_top) { return n_top == 0 ? 0 : n_top == 1 ? 1 : n_top <= 8 ? 8 : 32; }
 
 int stats_tiles(bool bf16, int V) {
@@ -406,9 +407,10 @@ int stats_tiles(bool bf16, int V) {
 
 namespace {
 
-// Calls of up to this many positions join each one's tiles by a block, larger ones by a warp: 300 positions over
-// V = 32,000 take 64.5 us in all with blocks and 66.8 us with warps, 1,000 take 114 us with either,
-// 8,000 take 584 us and 550 us.
+// Calls of up to this many positions join each one's tiles by a block, larger ones by a warp. In all, at
+// V = 32,000, d = 512, with 0 / 8 / 20 alternatives: 300 positions 25.6 / 57 / 120 us by blocks and
+// 27.5 / 59 / 128 us by warps, 1,000 44 / 89 / 206 and 44 / 89 / 208, 2,000 75 / 145 / 359 and
+// 73 / 139 / 349, 8,000 243 / 477 / 1189 and 235 / 446 / 1131.
 constexpr int kBlockJoin = 1024;
 
 template <int K>

@@ -12,7 +12,7 @@
 //
 // HBM bounds it: one position at V = 128,256, d = 4096 takes 158 us (6.6 TB/s), with 8 alternatives
 // and the join 168 us; 48 positions at V = 151,936, d = 2048 take 103 us, 110 us with 8
-// alternatives, 125 us with 20 (the lists' upkeep, see kBidGroups).
+// alternatives, 121 us with 20 (the lists' upkeep, see kBidGroups).
 //
 // Roles (320 threads): warp 0 issues the TMA loads, warp 1 owns TMEM and issues the MMAs, warps
 // 2-9 turn the accumulator around through shared memory (z[position][vocabulary row]); then each
