@@ -138,14 +138,17 @@ constexpr int kSegRows = kSRows / kSSegs;
 // equal (stats_stream_rows).
 struct StreamSplit {
   int V, ctas, rows;
-  __device__ __forceinline__ int tiles(int cta) const {
+  __host__ __device__ __forceinline__ int tiles(int cta) const {
     const int all = (V + rows - 1) / rows;
     return cta < all ? (all - cta + ctas - 1) / ctas : 0;
   }
-  __device__ __forceinline__ int first(int cta, int t) const { return (t * ctas + cta) * rows; }
-  // The list of vocabulary row v: its CTA's, of the segment its row of the tile falls into.
-  __device__ __forceinline__ int list_of(int v) const {
-    return v / rows % ctas * kSSegs + v % rows / kSegRows;
+  __host__ __device__ __forceinline__ int first(int cta, int t) const { return (t * ctas + cta) * rows; }
+  // The list of vocabulary row v: its CTA's, of the segment its row of the tile falls into. In unsigned
+  // arithmetic any v names one of the ctas * kSSegs lists: after a wait that ran out a CTA has
+  // left its lists unwritten, and the join looks up ids that an earlier use of the workspace left.
+  __host__ __device__ __forceinline__ int list_of(int v) const {
+    const unsigned u = static_cast<unsigned>(v), r = static_cast<unsigned>(rows);
+    return static_cast<int>(u / r % static_cast<unsigned>(ctas) * kSSegs + u % r / kSegRows);
   }
 };
 
