@@ -655,8 +655,9 @@ int dpo::device_sms() {
 }
 
 bool dpo::current_context(void** ctx) {
-  // The runtime's calls above made the device's primary context current; the driver's
-  // cuCtxGetCurrent (reached without linking libcuda) names it.
+  // The driver's cuCtxGetCurrent (reached without linking libcuda) names the context. A host
+  // thread that has made no CUDA call that needs one has none yet: choosing its device again
+  // makes the primary context current.
   static PFN_cuCtxGetCurrent_v4000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -668,7 +669,12 @@ bool dpo::current_context(void** ctx) {
   });
   if (fn == nullptr) return false;
   CUcontext c = nullptr;
-  if (fn(&c) != CUDA_SUCCESS || c == nullptr) return false;
+  if (fn(&c) != CUDA_SUCCESS) return false;
+  if (c == nullptr) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return false;
+    if (fn(&c) != CUDA_SUCCESS || c == nullptr) return false;
+  }
   *ctx = c;
   return true;
 }
