@@ -105,12 +105,15 @@ inline int short_lanes(int d) {
   return g;
 }
 
+// Lets a kernel ask for `bytes` of dynamic shared memory. The limit is the kernel's, not the launch's: it
+// is set to the most any length takes, so that a call of another thread in between cannot leave it
+// below this launch's.
 template <class Kern>
 cudaError_t allow_smem(Kern kern, size_t bytes) {
   // 48 KiB without asking, static shared memory included
-  return bytes > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  static_cast<int>(bytes))
-                           : cudaSuccess;
+  return bytes > 40 * 1024
+             ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)
+             : cudaSuccess;
 }
 
 inline RowsQ8 held_rows(const NormIn& n) { return RowsQ8{n.codes, n.scales, n.d, q_blocks(n.d)}; }
