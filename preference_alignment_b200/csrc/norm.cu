@@ -8,7 +8,7 @@
 //   dw = sum over rows of dy xh, db = sum over rows of dy
 //
 // The forward: 16,384 rows of 4,096 in bf16 take 45.7 us (5.9 TB/s; 48 to 50 in calls one after
-// another), 67 us when they are held in 8 bits too. No unit is full (issue slots 49 % and the shared-memory pipe 66 % of the time, ncu): four warps
+// another), 65 us when they are held in 8 bits too. No unit is full (issue slots 49 % and the shared-memory pipe 66 % of the time, ncu): four warps
 // per scheduler, all that its registers leave, do not cover the waits for shared memory (the slot, the
 // weight and bias in fp32, the exchanges of the row sums), 2.9 of 8.1 cycles per instruction.
 //
